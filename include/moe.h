@@ -31,6 +31,12 @@
  *            hardware", measured-benchmark table and community remarks: the
  *            --topp 0.7 setting loads fewer experts per token (1.6x end to
  *            end on a RAM-bound machine).
+ *  [P-mla]   agentlenshq.com, "Colibri: running GLM-5.2 744B MoE on consumer
+ *            hardware", section "Key features": attention over a compressed
+ *            cache (32,768 -> 576 floats a token) and weight absorption, which
+ *            removes the per-token reconstruction of keys and values.
+ *  [P-mtp]   tech.takumi3488.com, "Trying colibri", the MTP section: drafted
+ *            tokens are verified together.
  *
  * Conventions for every call:
  *  - Tensor pointers are DEVICE pointers (hipMalloc'd or torch CUDA tensors)
@@ -463,6 +469,109 @@ int moe_pool_resident_bits(const moe_pool *pool, int layer, int expert);
 moe_status moe_pool_stats(const moe_pool *pool, uint64_t *hits, uint64_t *misses, uint64_t *bytes_h2d);
 /* 1 if (layer, expert) is resident, 0 if not, -1 for invalid arguments. */
 int moe_pool_resident(const moe_pool *pool, int layer, int expert);
+
+/* ---------------------------------------------------------------------- */
+/* Latent attention ([P-mla], [P-mtp])                                    */
+/* ---------------------------------------------------------------------- */
+
+/* Attention whose cache holds one row a token for all heads: a latent c
+ * (d_latent values) and a rotary key k (d_rope values). Head h has expansion
+ * weights W_k (d_nope x d_latent) and W_v (d_v x d_latent); its key is
+ * [W_k c | k], its value W_v c, its query [q_nope | q_rope]:
+ *   s_j = scale (q_nope . W_k c_j + q_rope . k_j), p = softmax of s over the
+ *   visible j, out = W_v sum_j p_j c_j.
+ * Two forms of the same function:
+ *   absorbed (moe_latent_attend): a = W_k^T q_nope, s_j = scale [a | q_rope] .
+ *     [c_j | k_j], out = W_v (sum_j p_j c_j): the cache is read as it is, once
+ *     for all heads; for single tokens and drafts.
+ *   expanded (moe_latent_prompt): keys and values of every head are computed
+ *     from the cache first; fewer products when there are many queries.
+ *
+ * Elements (queries, cache, weights, out) are bf16 or fp16; scores, softmax
+ * statistics and every sum are fp32. Rounded to the element type on the way:
+ * a, the softmax weights before they multiply values, sum_j p_j c_j (both
+ * forms' last product takes elements), and the expanded keys and values.
+ *
+ * The cache is pages of page_size rows: [n_pages][page_size][d_latent +
+ * d_rope]. Sequence b has kv_len[b] cached rows, the call's own tokens last;
+ * row j is row j % page_size of page page_table[b][j / page_size]. Its queries
+ * are the tokens q_start[b] .. q_start[b+1] - 1 and stand at its last
+ * positions. Entries of the table behind a sequence's last row are not read.
+ *
+ * n_heads 1..128; d_latent 128, 256 or 512; d_rope 32 or 64; (d_nope, d_v)
+ * (64, 64), (128, 128) or (192, 256); page_size a power of two up to 65536;
+ * scale finite. */
+enum { MOE_BF16 = 0, MOE_FP16 = 1 };
+typedef struct {
+  int n_heads, d_latent, d_rope, d_nope, d_v;
+  int dtype; /* MOE_BF16 or MOE_FP16 */
+  int page_size;
+  float scale;
+} moe_latent_cfg;
+
+/* What both forms take. q_nope[t * nope_t + h * nope_h + i] (strides in
+ * elements, multiples of 8), q_rope likewise; all DEVICE pointers.
+ * T <= 2^20 tokens, B <= 1024 sequences. out [T][n_heads][d_v] may be no input.
+ * Checked on the device, reported by moe_ctx_check as MOE_EINVAL, without a
+ * read or write outside the arrays: q_start not ascending within 0..T, kv_len
+ * negative or above max_pages * page_size, page ids outside [0, n_pages) (the
+ * sequence's results are then unspecified). Tokens that belong to no sequence
+ * are not written. */
+typedef struct {
+  int T, B;
+  const void *q_nope;
+  int64_t nope_t, nope_h;
+  const void *q_rope;
+  int64_t rope_t, rope_h;
+  const void *cache;
+  int64_t n_pages;
+  const int32_t *page_table; /* [B][max_pages] */
+  int max_pages;
+  const int32_t *q_start; /* [B+1] */
+  const int32_t *kv_len;  /* [B] */
+  void *out;
+} moe_latent_call;
+
+/* Write T tokens into the cache: kv [T][d_latent + d_rope] (rows kv_t elements
+ * apart, a multiple of 8) holds a token's latent and its rotary key before
+ * their norm and rotation. slot[t] (DEVICE int64) is the row it goes to (page *
+ * page_size + row of the page), -1: nowhere; the slots of a call are distinct.
+ * Written: c * norm_w / sqrt(mean c^2 + eps) (norm_w fp32 [d_latent]; NULL: the
+ * latent as it is) and the key with its pairs (2i, 2i + 1) turned by the angle
+ * of position pos[t], whose cosine and sine are turn[pos][i][0..1] (fp32
+ * [n_pos][d_rope / 2][2]). With q_rope (strides rope_t, rope_h in elements,
+ * multiples of 8): also q_rope_out [T][n_heads][d_rope] = the queries' rotary
+ * parts turned the same way, for every token. Computed in fp32 and rounded
+ * once. A slot outside the cache or a position outside the table is reported
+ * by moe_ctx_check and the token skipped. cfg's d_nope, d_v and scale are not
+ * used. */
+moe_status moe_latent_append(moe_ctx *ctx, const moe_latent_cfg *cfg, int T, const void *kv, int64_t kv_t,
+                             const float *norm_w, float eps, const float *turn, int n_pos, const int32_t *pos,
+                             const int64_t *slot, void *cache, int64_t n_pages, const void *q_rope, int64_t rope_t,
+                             int64_t rope_h, void *q_rope_out);
+
+/* Absorbed form. w_kt [n_heads][d_latent][d_nope] (W_k transposed) and w_kv
+ * [n_heads][d_nope + d_v][d_latent] (W_k's rows, then W_v's; only W_v's are
+ * read). max_q: at least the largest number of queries of a sequence (a hint
+ * for the tiling; results do not depend on it but for rounding).
+ * Query i of n sees the cached rows before the call's own tokens and, with
+ * tree NULL, the call's own rows 0..i; with tree (DEVICE uint64 [T], n <= 64),
+ * own row j where bit j of its word is set (a longer tree is reported by
+ * moe_ctx_check; its rows from 64 on are seen by none of its own). A query that sees nothing gives
+ * zeros. What a query does not see has no part in its result, whatever it
+ * holds (NaN and infinities included).
+ * Nothing about the lengths is read on the host: a captured graph may be
+ * replayed on other lengths, tables and masks. */
+moe_status moe_latent_attend(moe_ctx *ctx, const moe_latent_cfg *cfg, const moe_latent_call *call, const void *w_kt,
+                             const void *w_kv, const uint64_t *tree, int max_q);
+
+/* Expanded form, causal: query i of n sees the rows 0 .. kv_len - n + i. n_kv:
+ * at least the sum of kv_len (sizes the expansion's workspace of n_kv *
+ * n_heads * (d_nope + d_v) elements; a larger sum is reported by moe_ctx_check
+ * and the sequences beyond it are not computed). Other arguments and rules as
+ * above. */
+moe_status moe_latent_prompt(moe_ctx *ctx, const moe_latent_cfg *cfg, const moe_latent_call *call, const void *w_kv,
+                             int64_t n_kv);
 
 /* ---------------------------------------------------------------------- */
 /* Measurement                                                            */

@@ -56,6 +56,20 @@ class DebugBufs(ctypes.Structure):
                 ("aq", ctypes.c_void_p), ("sa", ctypes.c_void_p), ("accd", ctypes.c_void_p)]
 
 
+class _LatentCfg(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int), ("d_latent", ctypes.c_int), ("d_rope", ctypes.c_int),
+                ("d_nope", ctypes.c_int), ("d_v", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class _LatentCall(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("B", ctypes.c_int), ("q_nope", ctypes.c_void_p), ("nope_t", ctypes.c_int64),
+                ("nope_h", ctypes.c_int64), ("q_rope", ctypes.c_void_p), ("rope_t", ctypes.c_int64),
+                ("rope_h", ctypes.c_int64), ("cache", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("max_pages", ctypes.c_int), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("out", ctypes.c_void_p)]
+
+
 # name -> (restype, argtypes)
 _vp, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _SIGS = {
@@ -109,6 +123,10 @@ _SIGS = {
     "moe_pool_layer_table": (_i32, [_vp, _i32, ctypes.POINTER(_vp), ctypes.POINTER(_vp)]),
     "moe_layer_forward_noalloc": (_i32, [_vp, _i32, ctypes.POINTER(RouterCfg), _vp, _vp, _vp, _vp, _vp,
                                          ctypes.POINTER(ExpertW), _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_latent_append": (_i32, [_vp, ctypes.POINTER(_LatentCfg), _i32, _vp, _i64, _vp, _f32, _vp, _i32, _vp, _vp, _vp,
+                                 _i64, _vp, _i64, _i64, _vp]),
+    "moe_latent_attend": (_i32, [_vp, ctypes.POINTER(_LatentCfg), ctypes.POINTER(_LatentCall), _vp, _vp, _vp, _i32]),
+    "moe_latent_prompt": (_i32, [_vp, ctypes.POINTER(_LatentCfg), ctypes.POINTER(_LatentCall), _vp, _i64]),
 }
 
 
@@ -436,6 +454,115 @@ def _layer(name, ctx, bits, x, table, shared, k, I, out, w_router, bias, logits,
                              None if logits is not None else w_router.data_ptr(), _ptr(bias), table.data_ptr(), sh,
                              T, H, I, out.data_ptr(), _ptr(topk_idx), _ptr(topk_w), _ptr(xq), _ptr(sx),
                              _ptr(y_slots)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Latent attention
+# ---------------------------------------------------------------------------
+
+class LatentCfg:
+    """moe_latent_cfg: head and cache layout of one latent-attention layer.
+    dtype: torch.bfloat16 or torch.float16 (queries, cache, weights, out)."""
+
+    def __init__(self, n_heads: int, d_latent: int, d_rope: int, d_nope: int, d_v: int,
+                 dtype: torch.dtype = torch.bfloat16, page_size: int = 64, scale: float | None = None):
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
+        self.n_heads, self.d_latent, self.d_rope, self.d_nope, self.d_v = n_heads, d_latent, d_rope, d_nope, d_v
+        self.dtype, self.page_size = dtype, page_size
+        self.scale = (d_nope + d_rope) ** -0.5 if scale is None else float(scale)
+        self.struct = _LatentCfg(n_heads, d_latent, d_rope, d_nope, d_v, 0 if dtype == torch.bfloat16 else 1,
+                                 page_size, self.scale)
+        self.ref = ctypes.byref(self.struct)
+
+
+def _rows3(t: torch.Tensor, dtype, name, shape):
+    """A [T][H][d] view whose rows are contiguous: (address, token stride, head stride)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
+    st, sh, s1 = t.stride()
+    if s1 != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # the stride of an axis of one entry is never used, and may be anything
+    return t.data_ptr(), st if shape[0] > 1 else 0, sh if shape[1] > 1 else 0
+
+
+def moe_latent_append(ctx: MoeCtx, cfg: LatentCfg, kv: torch.Tensor, turn: torch.Tensor, pos: torch.Tensor,
+                      slot: torch.Tensor, cache: torch.Tensor, norm_w: torch.Tensor | None = None, eps: float = 1e-6,
+                      q_rope: torch.Tensor | None = None, q_rope_out: torch.Tensor | None = None):
+    """Norm and rotate T tokens into the cache (see include/moe.h). kv [T][d_latent
+    + d_rope] (rows may be strided), turn fp32 [n_pos][d_rope/2][2], pos int32
+    [T], slot int64 [T] (-1: not kept), cache [n_pages][page][d_latent + d_rope];
+    q_rope [T][H][d_rope] (a strided view is fine) is rotated into q_rope_out."""
+    T, row = kv.shape[0], cfg.d_latent + cfg.d_rope
+    if not kv.is_cuda or kv.dtype != cfg.dtype:
+        raise TypeError(f"kv must be a CUDA (HIP) {cfg.dtype} tensor")
+    if kv.shape != (T, row) or kv.stride(1) != 1:
+        raise ValueError(f"kv must be [T][{row}] with contiguous rows")
+    _dev(turn, torch.float32, "turn", (turn.shape[0], cfg.d_rope // 2, 2))
+    _dev(pos, torch.int32, "pos", (T,))
+    _dev(slot, torch.int64, "slot", (T,))
+    _dev(cache, cfg.dtype, "cache", (cache.shape[0], cfg.page_size, row))
+    if norm_w is not None:
+        _dev(norm_w, torch.float32, "norm_w", (cfg.d_latent,))
+    qr, qt, qh = None, 0, 0
+    if q_rope is not None:
+        shape = (T, cfg.n_heads, cfg.d_rope)
+        qr, qt, qh = _rows3(q_rope, cfg.dtype, "q_rope", shape)
+        if q_rope_out is None:
+            raise ValueError("q_rope needs q_rope_out")
+        _dev(q_rope_out, cfg.dtype, "q_rope_out", shape)
+    elif q_rope_out is not None:
+        raise ValueError("q_rope_out needs q_rope")
+    _ck(lib().moe_latent_append(ctx.handle, cfg.ref, T, kv.data_ptr(), kv.stride(0) if T > 1 else row, _ptr(norm_w),
+                                eps, turn.data_ptr(), turn.shape[0], pos.data_ptr(), slot.data_ptr(),
+                                cache.data_ptr(), cache.shape[0], qr, qt, qh, _ptr(q_rope_out)))
+    return cache
+
+
+def _latent_call(cfg, q_nope, q_rope, w_kv, cache, table, q_start, kv_len, out):
+    T, B, H = q_nope.shape[0], kv_len.shape[0], cfg.n_heads
+    qn, nt, nh = _rows3(q_nope, cfg.dtype, "q_nope", (T, H, cfg.d_nope))
+    qr, rt, rh = _rows3(q_rope, cfg.dtype, "q_rope", (T, H, cfg.d_rope))
+    _dev(w_kv, cfg.dtype, "w_kv", (H, cfg.d_nope + cfg.d_v, cfg.d_latent))
+    _dev(cache, cfg.dtype, "cache", (cache.shape[0], cfg.page_size, cfg.d_latent + cfg.d_rope))
+    _dev(table, torch.int32, "table", (B, table.shape[1]))
+    _dev(q_start, torch.int32, "q_start", (B + 1,))
+    _dev(kv_len, torch.int32, "kv_len", (B,))
+    _dev(out, cfg.dtype, "out", (T, H, cfg.d_v))
+    return _LatentCall(T, B, qn, nt, nh, qr, rt, rh, cache.data_ptr(), cache.shape[0], table.data_ptr(),
+                       table.shape[1], q_start.data_ptr(), kv_len.data_ptr(), out.data_ptr())
+
+
+def moe_latent_attend(ctx: MoeCtx, cfg: LatentCfg, q_nope: torch.Tensor, q_rope: torch.Tensor, w_kt: torch.Tensor,
+                      w_kv: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, q_start: torch.Tensor,
+                      kv_len: torch.Tensor, max_q: int, out: torch.Tensor, tree: torch.Tensor | None = None):
+    """Absorbed form over the paged cache (see include/moe.h): q_nope
+    [T][H][d_nope] and q_rope [T][H][d_rope] (strided views are fine), w_kt
+    [H][d_latent][d_nope], w_kv [H][d_nope + d_v][d_latent], table int32
+    [B][max_pages], q_start int32 [B+1], kv_len int32 [B], out [T][H][d_v];
+    tree: int64 [T], each token's visible own rows as bits (NULL: causal)."""
+    call = _latent_call(cfg, q_nope, q_rope, w_kv, cache, table, q_start, kv_len, out)
+    _dev(w_kt, cfg.dtype, "w_kt", (cfg.n_heads, cfg.d_latent, cfg.d_nope))
+    if tree is not None:
+        _dev(tree, torch.int64, "tree", (call.T,))
+    _ck(lib().moe_latent_attend(ctx.handle, cfg.ref, ctypes.byref(call), w_kt.data_ptr(), w_kv.data_ptr(),
+                                _ptr(tree), max_q))
+    return out
+
+
+def moe_latent_prompt(ctx: MoeCtx, cfg: LatentCfg, q_nope: torch.Tensor, q_rope: torch.Tensor, w_kv: torch.Tensor,
+                      cache: torch.Tensor, table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+                      n_kv: int, out: torch.Tensor):
+    """Expanded form, causal (see include/moe.h): arguments as for
+    moe_latent_attend; n_kv: at least the sum of kv_len."""
+    call = _latent_call(cfg, q_nope, q_rope, w_kv, cache, table, q_start, kv_len, out)
+    _ck(lib().moe_latent_prompt(ctx.handle, cfg.ref, ctypes.byref(call), w_kv.data_ptr(), n_kv))
     return out
 
 

@@ -263,6 +263,9 @@ extern "C" moe_status moe_ctx_check(moe_ctx *ctx) {
     MOE_HIP(hipMemcpy(ctx->dev_small, &zero, sizeof zero, hipMemcpyHostToDevice));
     if (flags & ERRF_TIMEOUT) return moe_fail(MOE_ETIMEOUT, "device: a bounded wait gave up (flags 0x%x)", flags);
     if (flags & ERRF_BAD_INDEX) return moe_fail(MOE_EINVAL, "device: expert index out of range (flags 0x%x)", flags);
+    if (flags & ERRF_LATENT)
+      return moe_fail(MOE_EINVAL, "device: latent attention: page, slot, position or sequence bound out of range "
+                      "(flags 0x%x)", flags);
     return moe_fail(MOE_EINVAL, "device: error flags 0x%x", flags);
   }
   return MOE_OK;

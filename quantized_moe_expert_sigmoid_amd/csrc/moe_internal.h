@@ -18,6 +18,7 @@ enum : uint32_t {
   ERRF_BAD_INDEX = 1u << 0,  // an expert index outside [0, E)
   ERRF_TIMEOUT = 1u << 1,    // a bounded wait gave up
   ERRF_RANGE = 1u << 2,      // an int32 accumulator bound was exceeded
+  ERRF_LATENT = 1u << 3,     // latent attention: a page, slot, position or sequence bound out of range
 };
 
 struct moe_ctx {

@@ -45,8 +45,10 @@ FLAGS = [
 # ordinary VGPRs: with the default accumulation registers the compiler rotates
 # the loop-carried accumulators between them every K slice (about two
 # register moves per MFMA), which left the vector ALU as busy as the matrix
-# cores.
+# cores. The latent attention names its accumulators' registers itself; the
+# scores, which vector instructions work on, belong in VGPRs.
 FILE_FLAGS = {
+    "latent_attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "ffn_mfma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 

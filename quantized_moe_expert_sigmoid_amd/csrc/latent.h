@@ -40,23 +40,145 @@ moe_status launch_latent_append(moe_ctx *ctx, int dtype, const LatentAppendArgs 
 moe_status launch_latent_attend(moe_ctx *ctx, int dtype, const LatentArgs &a, int max_q);
 moe_status launch_latent_prompt(moe_ctx *ctx, int dtype, const LatentArgs &a, int64_t n_kv);
 
+// C[m][h][n] = sum_k A[m][h][k] B[h][n][k]; element (m, h, 0) of A at m a_m + h
+// a_h, of C at m c_m + h c_h; B's heads b_h apart. K and N are multiples of 64.
+struct HeadGemm {
+  const uint16_t *A, *B;
+  uint16_t *C;
+  const int64_t *rows;      // nullable: A's row of m
+  const int32_t *lo, *hi;   // nullable, on the device: only rows lo <= m < hi
+  int M, N, K;
+  int64_t a_m, a_h, b_h, c_m, c_h;
+};
+moe_status launch_head_gemm(moe_ctx *ctx, int dtype, const HeadGemm &g, int H);
+
 #if defined(__HIPCC__)
 
+typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
+typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
 // bf16 and fp16 elements: conversions round to nearest even, NaN stays NaN.
+// mfma: c += a b with v_mfma_f32_32x32x16: lane l holds 8 consecutive k of
+// row (a) or column (b) l % 32, k = 8 (l / 32) ..; of c it holds column l % 32,
+// rows 8 (i / 4) + 4 (l / 32) + i % 4 for i = 0..15.
 struct Bf16 {
-  uint16_t u;
+  static constexpr int kDtype = MOE_BF16;
+  static constexpr uint32_t kExp = 0x7f80;  // exponent bits
   static __device__ __forceinline__ float to_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-  static __device__ __forceinline__ uint16_t from_f32(float f) {
-    return __builtin_bit_cast(uint16_t, (__bf16)f);
+  static __device__ __forceinline__ uint16_t from_f32(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+  static __device__ __forceinline__ u16x8 from_f32x8(f32x8 f) {
+    return __builtin_bit_cast(u16x8, __builtin_convertvector(f, bf16x8));
+  }
+  static __device__ __forceinline__ f32x16 mfma(u16x8 a, u16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
   }
 };
 struct Fp16 {
-  uint16_t u;
+  static constexpr int kDtype = MOE_FP16;
+  static constexpr uint32_t kExp = 0x7c00;
   static __device__ __forceinline__ float to_f32(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
-  static __device__ __forceinline__ uint16_t from_f32(float f) {
-    return __builtin_bit_cast(uint16_t, (_Float16)f);
+  static __device__ __forceinline__ uint16_t from_f32(float f) { return __builtin_bit_cast(uint16_t, (_Float16)f); }
+  static __device__ __forceinline__ u16x8 from_f32x8(f32x8 f) {
+    return __builtin_bit_cast(u16x8, __builtin_convertvector(f, f16x8));
+  }
+  static __device__ __forceinline__ f32x16 mfma(u16x8 a, u16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
   }
 };
+
+// Accumulators kept in the accumulation registers (AGPRs) whatever else a
+// kernel holds. With ordinary variables the compiler moves such an array to
+// vector registers wherever vector instructions touch it (256 of them at once,
+// which spills); here every access names the class. The compiler does not see
+// matrix instructions inside assembly, so the waits it would add stand here: two
+// wait states from a vector write to a product that reads it, and settle()
+// before the accumulators are read back.
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass does not know the register class
+template <typename E>
+struct AccTile {
+  f32x16 c;
+  __device__ __forceinline__ void mfma(u16x8 a, u16x8 b) {
+    if constexpr (E::kDtype == MOE_BF16)
+      asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+    else
+      asm("s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+  }
+  __device__ __forceinline__ void scale(float f) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float x = c[e], t;
+      asm("v_accvgpr_read_b32 %1, %0\n\tv_mul_f32 %1, %1, %2\n\tv_accvgpr_write_b32 %0, %1"
+          : "+a"(x), "=&v"(t)
+          : "v"(f));
+      c[e] = x;
+    }
+  }
+  __device__ __forceinline__ float get(int e) const {
+    float x;
+    asm("v_accvgpr_read_b32 %0, %1" : "=v"(x) : "a"(c[e]));
+    return x;
+  }
+  __device__ __forceinline__ f32x4 get4(int j) const { return f32x4{get(4 * j), get(4 * j + 1), get(4 * j + 2), get(4 * j + 3)}; }
+};
+template <typename E, int N>
+__device__ __forceinline__ void settle(AccTile<E> (&t)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+a"(t[i].c));
+  asm volatile("s_nop 15\n\ts_nop 15");  // a 32x32x16 product's result is readable after at most 18 states
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+a"(t[i].c));
+}
+template <typename E, int N>
+__device__ __forceinline__ void clear(AccTile<E> (&t)[N]) {
+  const u16x8 z = {};
+#pragma unroll
+  for (int i = 0; i < N; ++i)  // volatile: a product each, not one value copied about
+    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %1, 0" : "=a"(t[i].c) : "v"(z));
+  settle(t);
+}
+#else
+template <typename E>
+struct AccTile {
+  __device__ void mfma(u16x8 a, u16x8 b);
+  __device__ void scale(float f);
+  __device__ float get(int e) const;
+  __device__ f32x4 get4(int j) const;
+};
+template <typename E, int N>
+__device__ void settle(AccTile<E> (&t)[N]);
+template <typename E, int N>
+__device__ void clear(AccTile<E> (&t)[N]);
+#endif
+
+// Transposed 8-byte LDS read (ds_read_b64_tr_b16): within 16 lanes, lane 4 e +
+// i's address is that of 4 elements of row e, columns 4 i ..; lane c receives
+// column c of rows 0..3.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u16x4 lds_read_tr(const uint8_t *p) {
+  return __builtin_bit_cast(u16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                       (__attribute__((address_space(3))) s16x4 *)(p)));
+}
+// 16 bytes a lane from global memory straight into LDS, 1 KB a wave: lane i's
+// go to LDS byte to + 16 i. Written in assembly because the compiler, which
+// does not follow which LDS bytes such a load writes, would wait for all of
+// them before any LDS read; there is no result register, and the caller waits
+// for the loads by count (vmcnt) before the barrier behind which they are read.
+// _s: a wave's common address and a lane's offset; _v: an address a lane.
+__device__ __forceinline__ void lds_load16_s(const void *base, uint32_t off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(to)
+               : "memory");
+}
+__device__ __forceinline__ void lds_load16_v(const void *p, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(to) : "memory");
+}
 
 // A sequence's bounds, made safe: tokens [t0, t0 + nq) of the call, len cached
 // rows, the first `before` of them older than the call (negative when the
@@ -64,6 +186,11 @@ struct Fp16 {
 struct LatentSeq {
   int t0, nq, len, before;
 };
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {
+  const uint64_t v = (uint64_t)p;
+  return (const uint8_t *)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
 __device__ __forceinline__ LatentSeq latent_seq(const LatentArgs &a, int b) {
   const int lo = a.q_start[b], hi = a.q_start[b + 1], n = a.kv_len[b];
   const int64_t cap = (int64_t)a.max_pages << a.page_shift;

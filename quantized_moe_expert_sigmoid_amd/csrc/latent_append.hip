@@ -5,7 +5,6 @@
 
 namespace {
 
-typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
 constexpr int kWaves = 4;
 
 // One 16-byte unit: pairs (2i, 2i + 1), i = 0..3, turned by (cos, sin) = turn[2i], turn[2i + 1].

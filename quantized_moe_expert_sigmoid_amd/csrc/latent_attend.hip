@@ -1,0 +1,482 @@
+// Latent attention, absorbed form: attention of every head over the cache's
+// rows as they are.
+//
+// Rows of queries (token i of a sequence, head h) are independent but share
+// every key and value, so a workgroup takes 32 WM rows of one sequence and a
+// run of its cache tiles of 32 tokens:
+//   S^T (tokens x rows) = K Q^T,  P^T = softmax,  O^T (latent x rows) += V^T P^T
+// with v_mfma_f32_32x32x16. A wave keeps 32 rows and 1 / WN of the latents of
+// O^T: a lane holds one row (l % 32) in S^T, P^T and O^T alike, so the running
+// maximum and sum are a lane's own registers and P^T feeds the second product
+// without leaving the lane (the tokens' order in the sum is free: both operands
+// take k slot (half, j) as token 4 half + j or, from j = 4 on, 8 + 4 half + j -
+// 4). The WN waves of a row group compute the same S^T: the repeated products
+// are cheaper than an exchange where the cache's bytes are the bound.
+#include "latent.h"
+
+#include <algorithm>
+#include <cmath>
+
+namespace {
+
+constexpr int kNT = 32;  // tokens of a cache tile
+
+// --- plan --------------------------------------------------------------------
+// A unit is one cache tile for one row tile. Units are numbered sequence by
+// sequence, row tile by row tile, cache tile by cache tile; workgroup w takes
+// units [w per, (w + 1) per), so that all have the same amount of work whatever
+// the lengths are. A row tile whose units several workgroups share is joined
+// from their partial results by the merge kernel.
+struct WgDesc {
+  int b, mt, kt, n;  // first unit, number of units
+};
+struct TileDesc {
+  int b, mt, w0, w1;  // row tile; the workgroups that share it
+  int64_t u0;
+};
+struct PlanHead {
+  int64_t per;
+  int n_tiles;
+};
+struct AttendWs {
+  PlanHead *head;
+  WgDesc *wg;
+  TileDesc *tile;
+  float *part;  // [2 n_wg][WM][dc / 32][4][64] x 4: O^T in the order of the lanes' registers
+  float2 *ml;   // [2 n_wg][32 WM]: running maximum and sum
+  uint16_t *q;  // [T][H][dc] absorbed queries
+  uint16_t *u;  // [T][H][dc] sums of latents
+};
+
+__device__ __forceinline__ int row_tiles(const LatentArgs &a, const LatentSeq &s, int mt) {
+  return (s.nq * a.H + mt - 1) / mt;
+}
+__device__ __forceinline__ int kv_tiles(const LatentSeq &s) { return max(1, (s.len + kNT - 1) / kNT); }
+
+template <typename T>
+__device__ T block_scan_excl(T v, T *tmp) {  // 1024 threads
+  const int i = threadIdx.x;
+  tmp[i] = v;
+  __syncthreads();
+  for (int o = 1; o < 1024; o <<= 1) {
+    const T x = i >= o ? tmp[i - o] : T(0);
+    __syncthreads();
+    tmp[i] += x;
+    __syncthreads();
+  }
+  const T r = tmp[i] - v;
+  __syncthreads();
+  return r;
+}
+
+__global__ __launch_bounds__(1024) void latent_plan_kernel(LatentArgs a, AttendWs ws, int mt, int n_wg, int min_per) {
+  __shared__ int64_t cum[1025];
+  __shared__ int64_t tmp[1024];
+  const int b = threadIdx.x;
+  LatentSeq s{};
+  if (b < a.B) s = latent_seq(a, b);
+  const int nt = b < a.B ? row_tiles(a, s, mt) : 0, kt = kv_tiles(s);
+  const int64_t units = (int64_t)nt * kt;
+  const int64_t u0 = block_scan_excl<int64_t>(units, tmp);
+  const int64_t t0 = block_scan_excl<int64_t>(nt, tmp);
+  cum[b] = u0;
+  if (b == 1023) cum[1024] = u0 + units;
+  __syncthreads();
+  const int64_t total = cum[1024];
+  const int64_t per = max((int64_t)min_per, (total + n_wg - 1) / n_wg);
+  if (b == 1023) {
+    ws.head->per = per;
+    ws.head->n_tiles = (int)(t0 + nt);
+  }
+  for (int i = 0; i < nt; ++i) {
+    const int64_t u = u0 + (int64_t)i * kt;
+    ws.tile[t0 + i] = TileDesc{b, i, (int)(u / per), (int)((u + kt - 1) / per), u};
+  }
+  for (int w = b; w < n_wg; w += 1024) {
+    const int64_t u = w * per;
+    WgDesc d{0, 0, 0, 0};
+    if (u < total) {
+      int lo = 0, hi = 1024;  // the last sequence with cum <= u that has units
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cum[mid] <= u) lo = mid; else hi = mid;
+      }
+      const LatentSeq q = latent_seq(a, lo);
+      const int k = kv_tiles(q);
+      const int64_t r = u - cum[lo];
+      d = WgDesc{lo, (int)(r / k), (int)(r % k), (int)min(per, total - u)};
+    }
+    ws.wg[w] = d;
+  }
+}
+
+// --- attention -----------------------------------------------------------------
+// A cache tile lies in LDS as panels of 64 columns: [panel][token][8 units of 16
+// bytes], a token's unit c at place c ^ swz(token). swz spreads 16 consecutive
+// tokens' equal units, and 4 tokens' runs of 4 units, over all 64 banks, which
+// is what the two products read at a time.
+__device__ __forceinline__ int swz(int token) { return ((token >> 1 & 1) << 2) | (token >> 2 & 3); }
+
+template <int DC, int DR, int WM, int WN>
+struct Attend {
+  static constexpr int kWaves = WM * WN, kMT = 32 * WM, kDK = DC + DR;
+  static constexpr int kPanels = (kDK + 63) / 64, kPanelB = kNT * 128, kTileB = kPanels * kPanelB;
+  static constexpr int kKS = kDK / 16;           // steps of the first product
+  static constexpr int kNB = DC / 32 / WN;       // blocks of 32 latents of a wave
+  // Steps whose query operand stays in LDS: O^T of 32 rows and 512 latents takes 256 registers a lane, and all 36
+  // steps' operands would take 144 of the other 256.
+  static constexpr int kQL = kNB >= 16 ? 12 : 0;
+  static constexpr int kBufs = kQL ? 3 : 4;      // tile buffers: one being read, the others in flight
+  static constexpr int kQB = kWaves * kQL * 1024;
+  static constexpr int kLds = kBufs * kTileB + kQB;
+  static_assert(kWaves == 4 && kLds <= 160 << 10, "4 waves load a tile's 32 tokens, 8 each");
+};
+
+// s_waitcnt vmcnt(n) alone
+#define WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (((n) >> 4) << 14) | (7 << 4) | (15 << 8))
+
+template <typename E, int DC, int DR, int WM, int WN>
+__global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, AttendWs ws, float c2, uint32_t flip) {
+  using C = Attend<DC, DR, WM, WN>;
+  constexpr int kNB = C::kNB, kBufs = C::kBufs, kPanels = C::kPanels;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLds];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN, l32 = lane & 31, hl = lane >> 5;
+  // neighbours in the unit order share cache rows: keep them on one XCD (ids go round the 8 XCDs)
+  const int w = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  const WgDesc d = ws.wg[w];
+  int b = uniform(d.b), mt = uniform(d.mt), kt = uniform(d.kt), left = uniform(d.n);
+  bool first = true;
+  const uint8_t *cache = static_cast<const uint8_t *>(a.cache);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
+
+  // lane constants of the three LDS access patterns
+  const int ld_row = lane >> 3;  // loads: token in the wave's block of 8
+  const int ld_unit = (lane & 7) ^ swz((8 * wave + ld_row) & 15);
+  // a last panel of 32 columns: its upper units repeat the lower ones
+  const int ld_last = C::kDK % 64 ? (ld_unit & 3) - ld_unit : 0;
+  int k_off[4], v_off[2][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) k_off[i] = l32 * 128 + (((2 * i + hl) ^ swz(l32 & 15)) << 4);
+  const int vt = 4 * hl + ((lane & 15) >> 2);  // token (mod 16) of the transposed reads; the second read is 8 on
+#pragma unroll
+  for (int h8 = 0; h8 < 2; ++h8)
+#pragma unroll
+    for (int p = 0; p < 2; ++p)  // the wave's first block of latents is an odd one where it has one alone
+      v_off[h8][p] = (vt + 8 * h8) * 128 +
+                     (((4 * (p ^ (kNB == 1 ? wn & 1 : 0)) + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ swz(vt + 8 * h8)) << 4) + (lane & 1) * 8;
+
+  while (left > 0) {
+    const LatentSeq r = latent_seq(a, b);
+    const LatentSeq s{uniform(r.t0), uniform(r.nq), uniform(r.len), uniform(r.before)};
+    const int nt = row_tiles(a, s, C::kMT), kts = kv_tiles(s);
+    const int n = min(left, kts - kt);
+    if (nt > 0) {
+      // the wave's rows
+      const int row = mt * C::kMT + wm * 32 + l32;
+      const bool live = row < s.nq * a.H;
+      const int qi = live ? row / a.H : 0, t = s.t0 + qi;
+      u16x8 q[C::kKS - C::kQL];
+      u16x8 *q_lds = reinterpret_cast<u16x8 *>(lds + kBufs * C::kTileB + wave * (C::kQL * 1024)) + lane;
+      {
+        const int h = live ? row - qi * a.H : 0;
+        const uint16_t *q1 = ws.q + ((int64_t)t * a.H + h) * DC + 8 * hl;
+        const uint16_t *q2 = static_cast<const uint16_t *>(a.q_rope) + t * a.rope_t + h * a.rope_h + 8 * hl;
+#pragma unroll
+        for (int k = 0; k < C::kKS; ++k) {
+          u32x4 v = {0, 0, 0, 0};
+          if (live) v = *reinterpret_cast<const u32x4 *>(16 * k < DC ? q1 + 16 * k : q2 + (16 * k - DC));
+          v ^= flip;
+          if (k < C::kQL)
+            q_lds[k * 64] = __builtin_bit_cast(u16x8, v);
+          else
+            q[k < C::kQL ? 0 : k - C::kQL] = __builtin_bit_cast(u16x8, v);
+        }
+      }
+      const uint64_t word = live && a.tree ? a.tree[t] : 0;
+      // the tokens of the tile from position j0 that the lane's row sees, as bits
+      auto seen = [&](int j0) {
+        const int old = min(max(s.before - j0, 0), 32), own = j0 - s.before;
+        uint32_t v = (uint32_t)((1ull << old) - 1);
+        if (a.tree)
+          v |= own >= 0 ? (uint32_t)(word >> min(own, 63)) & (own < 64 ? ~0u : 0u)
+                        : (uint32_t)(word << min(-own, 63)) & (own > -64 ? ~0u : 0u);
+        else
+          v = (uint32_t)((1ull << min(max(s.before + qi + 1 - j0, 0), 32)) - 1);
+        return v & (uint32_t)((1ull << min(max(s.len - j0, 0), 32)) - 1);
+      };
+
+      // The wave's 8 tokens of tile i of this run, into its buffer. Positions behind the sequence's last row repeat
+      // that row. Pages of 8 rows and more hold all 8: their id is a scalar load, which the count of outstanding
+      // vector loads does not see.
+      auto load = [&](int i) {
+        const int j0 = min((kt + i) * kNT + 8 * wave, (s.len - 1) & ~7);
+        const int r = min(ld_row, s.len - 1 - j0);
+        const uint32_t to = uniform(lds0 + (i % kBufs) * C::kTileB + wave * 1024);
+        if (a.page_shift >= 3) {
+          const int at = uniform(j0);
+          const int32_t *entry = a.page_table + (int64_t)b * a.max_pages + (at >> a.page_shift);
+          int page = uniform(*(const __attribute__((address_space(4))) int32_t *)(uintptr_t)entry);
+          if (page < 0 || page >= a.n_pages) {
+            if (lane == 0) atomicOr(a.err, (uint32_t)ERRF_LATENT);
+            page = 0;
+          }
+          const uint8_t *src =
+              uniform(cache + (((int64_t)page << a.page_shift) + (at & ((1 << a.page_shift) - 1))) * (C::kDK * 2));
+          const uint32_t off = r * (C::kDK * 2) + ld_unit * 16;
+#pragma unroll
+          for (int g = 0; g < kPanels; ++g)
+            lds_load16_s(uniform(src + g * 128), g == kPanels - 1 ? off + ld_last * 16 : off, to + g * C::kPanelB);
+        } else {
+          const uint8_t *src = cache + latent_row(a, b, j0 + r) * (C::kDK * 2) + ld_unit * 16;
+#pragma unroll
+          for (int g = 0; g < kPanels; ++g)
+            lds_load16_v(src + g * 128 + (g == kPanels - 1 ? ld_last * 16 : 0), to + g * C::kPanelB);
+        }
+      };
+
+      AccTile<E> acc[kNB];
+      clear(acc);
+      float m = -__builtin_inff(), l = 0.0f;
+      if (s.len > 0) {
+#pragma unroll
+        for (int i = 0; i < kBufs - 1; ++i)
+          if (i < n) load(i);
+        for (int it = 0; it < n; ++it) {
+          // the tile is complete when only the loads of later ones are outstanding
+          if (kBufs == 4 && it + 2 < n)
+            WAIT_VM(2 * kPanels);
+          else if (it + 1 < n)
+            WAIT_VM(kPanels);
+          else
+            WAIT_VM(0);
+          asm volatile("s_barrier" ::: "memory");  // for every wave's part of it; the oldest buffer's readers are done
+          if (it + kBufs - 1 < n) load(it + kBufs - 1);
+          uint8_t *kv = lds + (it % kBufs) * C::kTileB;
+          f32x16 z = {}, z1 = {};
+#pragma unroll
+          for (int k = 0; k < C::kKS; ++k) {
+            const u16x8 kf = *reinterpret_cast<const u16x8 *>(kv + k_off[k & 3] + (k >> 2) * C::kPanelB);
+            const u16x8 qf = k < C::kQL ? q_lds[k * 64] : q[k < C::kQL ? 0 : k - C::kQL];
+            if (k & 1)
+              z1 = E::mfma(kf, qf, z1);
+            else
+              z = E::mfma(kf, qf, z);
+          }
+          z += z1;
+          const int j0 = (kt + it) * kNT;
+          if (j0 + kNT > s.before) {  // the tile holds tokens that not every row sees
+            const uint32_t vis = seen(j0) >> (4 * hl);
+            bool odd = false;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const bool v = (vis >> (8 * (i >> 2) + (i & 3))) & 1;
+              odd |= !v & !(__builtin_fabsf(z[i]) < __builtin_inff());
+              z[i] = v ? z[i] : -__builtin_inff();
+            }
+            // An unseen row that holds NaN or infinities gives such a score, and would reach the sums as 0 x NaN or
+            // 0 x inf: then the tile's rows are looked through, the broken ones cleared for every wave, and the rows
+            // that do see one get a NaN sum.
+            if (__syncthreads_or(odd)) {
+              bool broken = false;
+#pragma unroll 1
+              for (int c = hl; c < DC / 8; c += 2) {
+                const u16x8 v = *reinterpret_cast<const u16x8 *>(kv + (c >> 3) * C::kPanelB + l32 * 128 +
+                                                                 (((c & 7) ^ swz(l32 & 15)) << 4));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) broken |= (v[e] & E::kExp) == E::kExp;
+              }
+              const uint64_t halves = __ballot(broken);
+              const uint32_t bad = (uint32_t)halves | (uint32_t)(halves >> 32);
+              __syncthreads();
+              if ((bad >> l32) & 1)
+#pragma unroll 1
+                for (int c = 2 * wave + hl; c < DC / 8; c += 8)
+                  *reinterpret_cast<u32x4 *>(kv + (c >> 3) * C::kPanelB + l32 * 128 +
+                                             (((c & 7) ^ swz(l32 & 15)) << 4)) = u32x4{0, 0, 0, 0};
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                z[i] = (bad >> (8 * (i >> 2) + 4 * hl + (i & 3))) & 1 ? -__builtin_inff() : z[i];
+              if (bad & (vis << (4 * hl))) l = __builtin_nanf("");
+              __syncthreads();
+            }
+          }
+          float top = z[0];
+#pragma unroll
+          for (int i = 1; i < 16; ++i) top = fmaxf(top, z[i]);
+          top = fmaxf(top, __shfl_xor(top, 32, 64)) * c2;
+          // The reference of the exponentials follows the maximum only when that has grown by 2^8: until then
+          // weights up to 2^8 are as exact as weights up to 1, and the sums need no rescaling.
+          if (__any(top > m + 8.0f)) {
+            const float mn = fmaxf(m, top);
+            const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < kNB; ++i) acc[i].scale(f);
+          }
+          const float base = m == -__builtin_inff() ? 0.0f : -m;
+          u16x8 p[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            f32x8 e;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[8 * half + i], c2, base));
+              l += e[i];
+            }
+            p[half] = E::from_f32x8(e);
+          }
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int nb = 0; nb < kNB; ++nb) {
+              const uint8_t *src = kv + ((wn * kNB + nb) >> 1) * C::kPanelB + ks * 16 * 128;
+              const u16x4 lo = lds_read_tr(src + v_off[0][nb & 1]), hi = lds_read_tr(src + v_off[1][nb & 1]);
+              acc[nb].mfma(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), p[ks]);
+            }
+        }
+      }
+      l += __shfl_xor(l, 32, 64);
+      settle(acc);
+      if (n == kts) {  // the whole row tile: finished here
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t *o = ws.u + ((int64_t)s.t0 * a.H + row) * DC + wn * (kNB * 32) + 4 * hl;
+        if (live)
+#pragma unroll
+          for (int i = 0; i < kNB; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              u16x4 v;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] = E::from_f32(acc[i].get(4 * j + e) * inv);
+              *reinterpret_cast<u16x4 *>(o + 32 * i + 8 * j) = v;
+            }
+      } else {
+        const int slot = 2 * w + (first ? 0 : 1);
+        float *o = ws.part + (((int64_t)slot * WM + wm) * WN + wn) * (kNB * 1024);
+#pragma unroll
+        for (int i = 0; i < kNB; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<f32x4 *>(o + ((i * 4 + j) * 64 + lane) * 4) = acc[i].get4(j);
+        if (hl == 0 && wn == 0) ws.ml[(int64_t)slot * C::kMT + wm * 32 + l32] = make_float2(m, l);
+      }
+      __syncthreads();  // the tiles are no longer read
+    }
+    first = false;
+    left -= nt > 0 ? n : 0;
+    kt = 0;
+    if (nt == 0 || ++mt == nt) {
+      mt = 0;
+      ++b;
+    }
+  }
+}
+
+// Join of the row tiles that several workgroups share: a wave takes one block
+// of 32 latents of 32 rows.
+template <typename E, int WM>
+__global__ __launch_bounds__(256) void latent_merge_kernel(LatentArgs a, AttendWs ws) {
+  const int ti = blockIdx.x / WM, wm = blockIdx.x % WM;
+  if (ti >= ws.head->n_tiles) return;
+  const TileDesc d = ws.tile[ti];
+  if (d.w0 == d.w1) return;
+  const int lane = threadIdx.x & 63, nb = blockIdx.y * 4 + (threadIdx.x >> 6), kNB = a.dc / 32;
+  const int l32 = lane & 31, hl = lane >> 5;
+  const LatentSeq s = latent_seq(a, d.b);
+  const int row = d.mt * 32 * WM + wm * 32 + l32;
+  const int64_t per = ws.head->per;
+  float m = -__builtin_inff(), l = 0.0f;
+  for (int w = d.w0; w <= d.w1; ++w) {
+    const int slot = 2 * w + (w * per >= d.u0 ? 0 : 1);
+    const float2 v = ws.ml[(int64_t)slot * 32 * WM + wm * 32 + l32];
+    const float mn = fmaxf(m, v.x);
+    l = l * (m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn)) + v.y * (v.x == mn ? 1.0f : __builtin_amdgcn_exp2f(v.x - mn));
+    m = mn;
+  }
+  f32x4 acc[4] = {};
+  for (int w = d.w0; w <= d.w1; ++w) {
+    const int slot = 2 * w + (w * per >= d.u0 ? 0 : 1);
+    const float mw = ws.ml[(int64_t)slot * 32 * WM + wm * 32 + l32].x;
+    const float f = mw == m ? 1.0f : __builtin_amdgcn_exp2f(mw - m);
+    const float *o = ws.part + ((int64_t)slot * WM + wm) * (kNB * 1024) + (nb * 4 * 64 + lane) * 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] += *reinterpret_cast<const f32x4 *>(o + j * 256) * f;
+  }
+  if (row >= s.nq * a.H) return;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t *o = ws.u + ((int64_t)s.t0 * a.H + row) * a.dc + 32 * nb + 4 * hl;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    u16x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = E::from_f32(acc[j][e] * inv);
+    *reinterpret_cast<u16x4 *>(o + 8 * j) = v;
+  }
+}
+
+template <typename E, int DC, int DR, int WM, int WN>
+moe_status launch(moe_ctx *ctx, const LatentArgs &a) {
+  using C = Attend<DC, DR, WM, WN>;
+  const int n_wg = ctx->n_cu / 8 * 8;  // a workgroup a CU: its buffers and accumulators fill one
+  const int64_t tiles = ((int64_t)a.T * a.H + C::kMT - 1) / C::kMT + a.B;
+  MoeLayout lay;
+  const size_t o_head = lay.take(sizeof(PlanHead)), o_wg = lay.take(sizeof(WgDesc) * n_wg),
+               o_tile = lay.take(sizeof(TileDesc) * tiles),
+               o_part = lay.take(sizeof(float) * 2 * n_wg * C::kMT * DC),
+               o_ml = lay.take(sizeof(float2) * 2 * n_wg * C::kMT),
+               o_q = lay.take(2 * (size_t)a.T * a.H * DC), o_u = lay.take(2 * (size_t)a.T * a.H * DC);
+  void *scr = nullptr;
+  moe_status st = moe_scratch(ctx, lay.size, &scr);
+  if (st) return st;
+  char *p = static_cast<char *>(scr);
+  const AttendWs ws{reinterpret_cast<PlanHead *>(p + o_head), reinterpret_cast<WgDesc *>(p + o_wg),
+                    reinterpret_cast<TileDesc *>(p + o_tile), reinterpret_cast<float *>(p + o_part),
+                    reinterpret_cast<float2 *>(p + o_ml),     reinterpret_cast<uint16_t *>(p + o_q),
+                    reinterpret_cast<uint16_t *>(p + o_u)};
+  hipLaunchKernelGGL(latent_plan_kernel, dim3(1), dim3(1024), 0, ctx->stream, a, ws, C::kMT, n_wg, 1);
+  MOE_CHECK_LAUNCH("latent_plan_kernel");
+  const int64_t hc = (int64_t)a.H * DC;
+  const HeadGemm absorb{static_cast<const uint16_t *>(a.q_nope), static_cast<const uint16_t *>(a.w_kt), ws.q, nullptr,
+                        nullptr, nullptr, a.T, DC, a.dn, a.nope_t, a.nope_h, (int64_t)DC * a.dn, hc, DC};
+  if ((st = launch_head_gemm(ctx, E::kDtype, absorb, a.H))) return st;
+  // The exponentials are powers of two of c2 z; a negative scale turns the queries' signs instead, and zero is
+  // taken as 1e-30 (weights of masked scores, -inf, must not meet 0 x inf).
+  const float c2 = std::max(std::fabs(a.scale) * 1.44269504088896340736f, 1e-30f);
+  hipLaunchKernelGGL((latent_attend_kernel<E, DC, DR, WM, WN>), dim3(n_wg), dim3(256), 0, ctx->stream, a, ws,
+                     c2, a.scale < 0 ? 0x80008000u : 0u);
+  MOE_CHECK_LAUNCH("latent_attend_kernel");
+  hipLaunchKernelGGL((latent_merge_kernel<E, WM>), dim3((unsigned)(tiles * WM), DC / 128), dim3(256), 0, ctx->stream,
+                     a, ws);
+  MOE_CHECK_LAUNCH("latent_merge_kernel");
+  const HeadGemm up{ws.u, static_cast<const uint16_t *>(a.w_kv) + (int64_t)a.dn * DC, static_cast<uint16_t *>(a.out),
+                    nullptr, a.q_start, a.q_start + a.B, a.T, a.dv, DC, hc, DC, (int64_t)(a.dn + a.dv) * DC,
+                    (int64_t)a.H * a.dv, a.dv};
+  return launch_head_gemm(ctx, E::kDtype, up, a.H);
+}
+
+template <typename E, int DC, int DR>
+moe_status pick(moe_ctx *ctx, const LatentArgs &a, int max_q) {
+  const int rows = std::max(1, max_q) * a.H;
+  if (rows <= 32) return launch<E, DC, DR, 1, 4>(ctx, a);
+  if (rows <= 64) return launch<E, DC, DR, 2, 2>(ctx, a);
+  return launch<E, DC, DR, 4, 1>(ctx, a);
+}
+
+template <typename E>
+moe_status attend(moe_ctx *ctx, const LatentArgs &a, int max_q) {
+  if (a.dr == 64)
+    return a.dc == 512   ? pick<E, 512, 64>(ctx, a, max_q)
+           : a.dc == 256 ? pick<E, 256, 64>(ctx, a, max_q)
+                         : pick<E, 128, 64>(ctx, a, max_q);
+  return a.dc == 512   ? pick<E, 512, 32>(ctx, a, max_q)
+         : a.dc == 256 ? pick<E, 256, 32>(ctx, a, max_q)
+                       : pick<E, 128, 32>(ctx, a, max_q);
+}
+
+}  // namespace
+
+moe_status launch_latent_attend(moe_ctx *ctx, int dtype, const LatentArgs &a, int max_q) {
+  return dtype == MOE_BF16 ? attend<Bf16>(ctx, a, max_q) : attend<Fp16>(ctx, a, max_q);
+}

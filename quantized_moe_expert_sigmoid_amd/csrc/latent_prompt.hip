@@ -1,80 +1,8 @@
-// Latent attention, both forms, in simple kernels: products of the heads'
-// weights with a tiled matrix-core kernel, attention with one workgroup a
-// query row.
+// Latent attention, expanded form: keys and values of every head computed from
+// the cache, then causal attention.
 #include "latent.h"
 
 namespace {
-
-typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-template <typename E>
-__device__ __forceinline__ f32x16 mfma32(u16x8 a, u16x8 b, f32x16 c);
-template <>
-__device__ __forceinline__ f32x16 mfma32<Bf16>(u16x8 a, u16x8 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
-                                                 0);
-}
-template <>
-__device__ __forceinline__ f32x16 mfma32<Fp16>(u16x8 a, u16x8 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
-                                                0);
-}
-
-// C[m][h][n] = sum_k A[m][h][k] B[h][n][k]; element (m, h, 0) of A at m a_m + h
-// a_h, of C at m c_m + h c_h; B's heads b_h apart. K and N are multiples of 64.
-struct HeadGemm {
-  const uint16_t *A, *B;
-  uint16_t *C;
-  const int64_t *rows;  // nullable: A's row of m
-  const int32_t *lo, *hi;  // nullable, on the device: only rows lo <= m < hi
-  int M, N, K;
-  int64_t a_m, a_h, b_h, c_m, c_h;
-};
-
-constexpr int kGT = 64;
-constexpr int kGPad = 8;
-
-template <typename E>
-__global__ __launch_bounds__(256) void head_gemm_kernel(HeadGemm g) {
-  __shared__ uint16_t as[kGT][kGT + kGPad], bs[kGT][kGT + kGPad];
-  const int M = g.hi ? min(g.M, *g.hi) : g.M, lo = g.lo ? *g.lo : 0;
-  const int m0 = blockIdx.x * kGT, n0 = blockIdx.y * kGT, h = blockIdx.z;
-  if (m0 >= M || m0 + kGT <= lo) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wn = (wave >> 1) * 32, wm = (wave & 1) * 32, l32 = lane & 31, hl = lane >> 5;
-  f32x16 acc = {};
-  for (int k0 = 0; k0 < g.K; k0 += kGT) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kGT * 8; i += 256) {
-      const int r = i >> 3, c = (i & 7) * 8;
-      const int m = min(m0 + r, M - 1);
-      *reinterpret_cast<u16x8 *>(&as[r][c]) =
-          *reinterpret_cast<const u16x8 *>(g.A + (g.rows ? g.rows[m] : m) * g.a_m + h * g.a_h + k0 + c);
-      *reinterpret_cast<u16x8 *>(&bs[r][c]) =
-          *reinterpret_cast<const u16x8 *>(g.B + h * g.b_h + (int64_t)(n0 + r) * g.K + k0 + c);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < kGT; kk += 16)
-      acc = mfma32<E>(*reinterpret_cast<const u16x8 *>(&bs[wn + l32][kk + 8 * hl]),
-                      *reinterpret_cast<const u16x8 *>(&as[wm + l32][kk + 8 * hl]), acc);
-  }
-  const int m = m0 + wm + l32;
-  if (m < lo || m >= M) return;
-  uint16_t *c = g.C + m * g.c_m + h * g.c_h + n0 + wn + 4 * hl;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) c[8 * (i >> 2) + (i & 3)] = E::from_f32(acc[i]);
-}
-
-template <typename E>
-moe_status head_gemm(moe_ctx *ctx, const HeadGemm &g, int H) {
-  hipLaunchKernelGGL(head_gemm_kernel<E>, dim3((g.M + kGT - 1) / kGT, g.N / kGT, H), dim3(256), 0, ctx->stream, g);
-  MOE_CHECK_LAUNCH("head_gemm_kernel");
-  return MOE_OK;
-}
 
 // The prompts' plan: off[b] = first expanded row of sequence b (B + 1 entries),
 // the expanded rows' cache rows. Sequences that do not fit n_kv rows are
@@ -185,29 +113,6 @@ __global__ __launch_bounds__(256) void attend_row_kernel(LatentArgs a, const uin
 }
 
 template <typename E>
-moe_status attend(moe_ctx *ctx, const LatentArgs &a) {
-  MoeLayout lay;
-  const size_t o_q = lay.take(2 * (size_t)a.T * a.H * a.dc), o_u = lay.take(2 * (size_t)a.T * a.H * a.dc);
-  void *scr = nullptr;
-  moe_status st = moe_scratch(ctx, lay.size, &scr);
-  if (st) return st;
-  uint16_t *q = reinterpret_cast<uint16_t *>((char *)scr + o_q), *u = reinterpret_cast<uint16_t *>((char *)scr + o_u);
-  const int64_t hc = (int64_t)a.H * a.dc;
-  if ((st = head_gemm<E>(ctx,
-                         HeadGemm{(const uint16_t *)a.q_nope, (const uint16_t *)a.w_kt, q, nullptr, nullptr, nullptr, a.T, a.dc,
-                                  a.dn, a.nope_t, a.nope_h, (int64_t)a.dc * a.dn, hc, a.dc},
-                         a.H)))
-    return st;
-  hipLaunchKernelGGL(attend_row_kernel<E>, dim3(a.T, a.H), dim3(256), 0, ctx->stream, a, q, hc, (int64_t)a.dc, a.dc,
-                     a.dc, nullptr, nullptr, 0, 0, nullptr, u, hc, (int64_t)a.dc);
-  MOE_CHECK_LAUNCH("attend_row_kernel");
-  return head_gemm<E>(ctx,
-                      HeadGemm{u, (const uint16_t *)a.w_kv + (int64_t)a.dn * a.dc, (uint16_t *)a.out, nullptr, a.q_start,
-                               a.q_start + a.B, a.T, a.dv, a.dc, hc, a.dc, (int64_t)(a.dn + a.dv) * a.dc, (int64_t)a.H * a.dv, a.dv},
-                      a.H);
-}
-
-template <typename E>
 moe_status prompt(moe_ctx *ctx, const LatentArgs &a, int64_t n_kv) {
   MoeLayout lay;
   const int dx = a.dn + a.dv;
@@ -225,7 +130,7 @@ moe_status prompt(moe_ctx *ctx, const LatentArgs &a, int64_t n_kv) {
   if (n_kv > 0) {
     hipLaunchKernelGGL(prompt_rows_kernel, dim3(16, a.B), dim3(256), 0, ctx->stream, a, off, rows);
     MOE_CHECK_LAUNCH("prompt_rows_kernel");
-    if ((st = head_gemm<E>(ctx,
+    if ((st = launch_head_gemm(ctx, E::kDtype,
                            HeadGemm{(const uint16_t *)a.cache, (const uint16_t *)a.w_kv, x, rows, nullptr, off + a.B, (int)n_kv,
                                     dx, a.dc, a.dc + a.dr, 0, (int64_t)dx * a.dc, hx, dx},
                            a.H)))
@@ -239,11 +144,6 @@ moe_status prompt(moe_ctx *ctx, const LatentArgs &a, int64_t n_kv) {
 }
 
 }  // namespace
-
-moe_status launch_latent_attend(moe_ctx *ctx, int dtype, const LatentArgs &a, int max_q) {
-  (void)max_q;
-  return dtype == MOE_BF16 ? attend<Bf16>(ctx, a) : attend<Fp16>(ctx, a);
-}
 
 moe_status launch_latent_prompt(moe_ctx *ctx, int dtype, const LatentArgs &a, int64_t n_kv) {
   return dtype == MOE_BF16 ? prompt<Bf16>(ctx, a, n_kv) : prompt<Fp16>(ctx, a, n_kv);

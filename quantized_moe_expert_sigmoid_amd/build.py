@@ -49,6 +49,7 @@ FLAGS = [
 # scores, which vector instructions work on, belong in VGPRs.
 FILE_FLAGS = {
     "latent_attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "latent_prompt.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "ffn_mfma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 

@@ -52,7 +52,18 @@ struct HeadGemm {
 };
 moe_status launch_head_gemm(moe_ctx *ctx, int dtype, const HeadGemm &g, int H);
 
+// The exponentials are powers of two of c2 z. A negative scale turns the
+// queries' signs instead, and zero is taken as 1e-30 (masked scores, -inf, must
+// not meet inf x 0).
+static inline float latent_c2(float scale) {
+  const float c = (scale < 0 ? -scale : scale) * 1.44269504088896340736f;
+  return c > 1e-30f ? c : 1e-30f;
+}
+
 #if defined(__HIPCC__)
+
+// s_waitcnt vmcnt(n) alone
+#define WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (((n) >> 4) << 14) | (7 << 4) | (15 << 8))
 
 typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));

@@ -15,7 +15,6 @@
 #include "latent.h"
 
 #include <algorithm>
-#include <cmath>
 
 namespace {
 
@@ -131,9 +130,6 @@ struct Attend {
   static constexpr int kLds = kBufs * kTileB + kQB;
   static_assert(kWaves == 4 && kLds <= 160 << 10, "4 waves load a tile's 32 tokens, 8 each");
 };
-
-// s_waitcnt vmcnt(n) alone
-#define WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (((n) >> 4) << 14) | (7 << 4) | (15 << 8))
 
 template <typename E, int DC, int DR, int WM, int WN>
 __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, AttendWs ws, float c2, uint32_t flip) {
@@ -441,9 +437,7 @@ moe_status launch(moe_ctx *ctx, const LatentArgs &a) {
   const HeadGemm absorb{static_cast<const uint16_t *>(a.q_nope), static_cast<const uint16_t *>(a.w_kt), ws.q, nullptr,
                         nullptr, nullptr, a.T, DC, a.dn, a.nope_t, a.nope_h, (int64_t)DC * a.dn, hc, DC};
   if ((st = launch_head_gemm(ctx, E::kDtype, absorb, a.H))) return st;
-  // The exponentials are powers of two of c2 z; a negative scale turns the queries' signs instead, and zero is
-  // taken as 1e-30 (weights of masked scores, -inf, must not meet 0 x inf).
-  const float c2 = std::max(std::fabs(a.scale) * 1.44269504088896340736f, 1e-30f);
+  const float c2 = latent_c2(a.scale);
   hipLaunchKernelGGL((latent_attend_kernel<E, DC, DR, WM, WN>), dim3(n_wg), dim3(256), 0, ctx->stream, a, ws,
                      c2, a.scale < 0 ? 0x80008000u : 0u);
   MOE_CHECK_LAUNCH("latent_attend_kernel");

@@ -1,6 +1,8 @@
 // Shared by the latent-attention kernels (latent*.hip, latent.cpp).
 #pragma once
 
+#include <type_traits>
+
 #include "moe_internal.h"
 
 // One call's arrays as the kernels see them (device pointers, strides in elements).
@@ -40,17 +42,40 @@ moe_status launch_latent_append(moe_ctx *ctx, int dtype, const LatentAppendArgs 
 moe_status launch_latent_attend(moe_ctx *ctx, int dtype, const LatentArgs &a, int max_q);
 moe_status launch_latent_prompt(moe_ctx *ctx, int dtype, const LatentArgs &a, int64_t n_kv);
 
+// How the absorbed form's work is shared out (see latent_attend.hip), written
+// by one workgroup of the kernel that absorbs the queries.
+struct WgDesc {
+  int b, mt, at, n;  // first unit: sequence, row tile, place in the row tile's units; number of units
+};
+struct TileDesc {
+  int b, mt, w0, w1;  // row tile; the workgroups that share its cache tiles
+  int64_t u0;         // its first unit
+};
+struct PlanHead {
+  int64_t per;  // units of a workgroup
+  int n_tiles;
+};
+struct LatentPlan {
+  LatentArgs a;
+  PlanHead *head;
+  WgDesc *wg;
+  TileDesc *tile;
+  int rows, tokens, over;  // rows of a row tile, tokens of a cache tile, units charged for starting a row tile
+  int n_wg;                // 0: no plan
+};
+
 // C[m][h][n] = sum_k A[m][h][k] B[h][n][k]; element (m, h, 0) of A at m a_m + h
-// a_h, of C at m c_m + h c_h; B's heads b_h apart. K and N are multiples of 64.
+// a_h, (m, h, n) of C at m c_m + h c_h + n / 16 c_n + n % 16; B's heads b_h
+// apart. K is a multiple of 64, N of 32.
 struct HeadGemm {
   const uint16_t *A, *B;
   uint16_t *C;
   const int64_t *rows;      // nullable: A's row of m
   const int32_t *lo, *hi;   // nullable, on the device: only rows lo <= m < hi
   int M, N, K;
-  int64_t a_m, a_h, b_h, c_m, c_h;
+  int64_t a_m, a_h, b_h, c_m, c_h, c_n;
 };
-moe_status launch_head_gemm(moe_ctx *ctx, int dtype, const HeadGemm &g, int H);
+moe_status launch_head_gemm(moe_ctx *ctx, int dtype, const HeadGemm &g, int H, const LatentPlan &plan);
 
 // The exponentials are powers of two of c2 z. A negative scale turns the
 // queries' signs instead, and zero is taken as 1e-30 (masked scores, -inf, must
@@ -61,6 +86,15 @@ static inline float latent_c2(float scale) {
 }
 
 #if defined(__HIPCC__)
+
+// f(integral_constant<int, A>) .. f(integral_constant<int, B - 1>)
+template <int A, int B, typename F>
+__device__ __forceinline__ void static_for(F &&f) {
+  if constexpr (A < B) {
+    f(std::integral_constant<int, A>{});
+    static_for<A + 1, B>(f);
+  }
+}
 
 // s_waitcnt vmcnt(n) alone
 #define WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (((n) >> 4) << 14) | (7 << 4) | (15 << 8))
@@ -169,6 +203,12 @@ template <typename E, int N>
 __device__ void clear(AccTile<E> (&t)[N]);
 #endif
 
+// Maximum of lanes l and l + 32, in both.
+__device__ __forceinline__ float max_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 // Transposed 8-byte LDS read (ds_read_b64_tr_b16): within 16 lanes, lane 4 e +
 // i's address is that of 4 elements of row e, columns 4 i ..; lane c receives
 // column c of rows 0..3.
@@ -182,13 +222,20 @@ __device__ __forceinline__ u16x4 lds_read_tr(const uint8_t *p) {
 // does not follow which LDS bytes such a load writes, would wait for all of
 // them before any LDS read; there is no result register, and the caller waits
 // for the loads by count (vmcnt) before the barrier behind which they are read.
-// _s: a wave's common address and a lane's offset; _v: an address a lane.
+// OFF is added to p and not to the place; on: -1, or 0 for a load that moves
+// nothing but is counted all the same. All lanes must be active.
+template <int OFF>
+__device__ __forceinline__ void lds_load16(const void *p, uint32_t to, int on = -1) {
+  // an instruction's offset counts on both sides
+  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b32 exec_lo, %2\n\ts_mov_b32 exec_hi, %2\n\t"
+               "global_load_lds_dwordx4 %0, off offset:%3\n\ts_mov_b64 exec, -1" ::"v"(p),
+               "s"(to - OFF), "s"(on), "n"(OFF)
+               : "memory");
+}
+// The same with a wave's common address and a lane's offset.
 __device__ __forceinline__ void lds_load16_s(const void *base, uint32_t off, uint32_t to) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(to)
                : "memory");
-}
-__device__ __forceinline__ void lds_load16_v(const void *p, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(to) : "memory");
 }
 
 // A sequence's bounds, made safe: tokens [t0, t0 + nq) of the call, len cached

@@ -15,99 +15,34 @@
 #include "latent.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace {
 
 constexpr int kNT = 32;  // tokens of a cache tile
 
-// --- plan --------------------------------------------------------------------
-// A unit is one cache tile for one row tile. Units are numbered sequence by
-// sequence, row tile by row tile, cache tile by cache tile; workgroup w takes
-// units [w per, (w + 1) per), so that all have the same amount of work whatever
-// the lengths are. A row tile whose units several workgroups share is joined
-// from their partial results by the merge kernel.
-struct WgDesc {
-  int b, mt, kt, n;  // first unit, number of units
-};
-struct TileDesc {
-  int b, mt, w0, w1;  // row tile; the workgroups that share it
-  int64_t u0;
-};
-struct PlanHead {
-  int64_t per;
-  int n_tiles;
-};
+// A unit of work is one cache tile for one row tile. Units are numbered sequence
+// by sequence, row tile by row tile, cache tile by cache tile, each row tile
+// with kOver units ahead of its cache tiles for what starting and ending it
+// costs; workgroup w takes units [w per, (w + 1) per), so that all have about
+// the same work whatever the lengths are. A row tile whose cache tiles several
+// workgroups share is joined from their partial results by the merge kernel.
+constexpr int kOver = 2;
+
 struct AttendWs {
-  PlanHead *head;
-  WgDesc *wg;
-  TileDesc *tile;
-  float *part;  // [2 n_wg][WM][dc / 32][4][64] x 4: O^T in the order of the lanes' registers
-  float2 *ml;   // [2 n_wg][32 WM]: running maximum and sum
-  uint16_t *q;  // [T][H][dc] absorbed queries
-  uint16_t *u;  // [T][H][dc] sums of latents
+  const PlanHead *head;
+  const WgDesc *wg;
+  const TileDesc *tile;
+  float *part;        // [2 n_wg][WM][dc / 32][4][64] x 4: O^T in the order of the lanes' registers
+  float2 *ml;         // [2 n_wg][32 WM]: running maximum and sum
+  const uint16_t *q;  // [dc / 16][T][H][16] absorbed queries: 32 rows' operand of a step is 1 KB in a row
+  uint16_t *u;        // [T][H][dc] sums of latents
 };
 
 __device__ __forceinline__ int row_tiles(const LatentArgs &a, const LatentSeq &s, int mt) {
   return (s.nq * a.H + mt - 1) / mt;
 }
 __device__ __forceinline__ int kv_tiles(const LatentSeq &s) { return max(1, (s.len + kNT - 1) / kNT); }
-
-template <typename T>
-__device__ T block_scan_excl(T v, T *tmp) {  // 1024 threads
-  const int i = threadIdx.x;
-  tmp[i] = v;
-  __syncthreads();
-  for (int o = 1; o < 1024; o <<= 1) {
-    const T x = i >= o ? tmp[i - o] : T(0);
-    __syncthreads();
-    tmp[i] += x;
-    __syncthreads();
-  }
-  const T r = tmp[i] - v;
-  __syncthreads();
-  return r;
-}
-
-__global__ __launch_bounds__(1024) void latent_plan_kernel(LatentArgs a, AttendWs ws, int mt, int n_wg, int min_per) {
-  __shared__ int64_t cum[1025];
-  __shared__ int64_t tmp[1024];
-  const int b = threadIdx.x;
-  LatentSeq s{};
-  if (b < a.B) s = latent_seq(a, b);
-  const int nt = b < a.B ? row_tiles(a, s, mt) : 0, kt = kv_tiles(s);
-  const int64_t units = (int64_t)nt * kt;
-  const int64_t u0 = block_scan_excl<int64_t>(units, tmp);
-  const int64_t t0 = block_scan_excl<int64_t>(nt, tmp);
-  cum[b] = u0;
-  if (b == 1023) cum[1024] = u0 + units;
-  __syncthreads();
-  const int64_t total = cum[1024];
-  const int64_t per = max((int64_t)min_per, (total + n_wg - 1) / n_wg);
-  if (b == 1023) {
-    ws.head->per = per;
-    ws.head->n_tiles = (int)(t0 + nt);
-  }
-  for (int i = 0; i < nt; ++i) {
-    const int64_t u = u0 + (int64_t)i * kt;
-    ws.tile[t0 + i] = TileDesc{b, i, (int)(u / per), (int)((u + kt - 1) / per), u};
-  }
-  for (int w = b; w < n_wg; w += 1024) {
-    const int64_t u = w * per;
-    WgDesc d{0, 0, 0, 0};
-    if (u < total) {
-      int lo = 0, hi = 1024;  // the last sequence with cum <= u that has units
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cum[mid] <= u) lo = mid; else hi = mid;
-      }
-      const LatentSeq q = latent_seq(a, lo);
-      const int k = kv_tiles(q);
-      const int64_t r = u - cum[lo];
-      d = WgDesc{lo, (int)(r / k), (int)(r % k), (int)min(per, total - u)};
-    }
-    ws.wg[w] = d;
-  }
-}
 
 // --- attention -----------------------------------------------------------------
 // A cache tile lies in LDS as panels of 64 columns: [panel][token][8 units of 16
@@ -122,9 +57,11 @@ struct Attend {
   static constexpr int kPanels = (kDK + 63) / 64, kPanelB = kNT * 128, kTileB = kPanels * kPanelB;
   static constexpr int kKS = kDK / 16;           // steps of the first product
   static constexpr int kNB = DC / 32 / WN;       // blocks of 32 latents of a wave
-  // Steps whose query operand stays in LDS: O^T of 32 rows and 512 latents takes 256 registers a lane, and all 36
+  // Every third step's query operand stays in LDS where O^T takes 256 registers a lane (32 rows of 512 latents): all
   // steps' operands would take 144 of the other 256.
-  static constexpr int kQL = kNB >= 16 ? 12 : 0;
+  static constexpr int kQL = kNB >= 16 ? kKS / 3 : 0;
+  static constexpr bool in_lds(int k) { return kQL && k % 3 == 2; }
+  static_assert(!kQL || kQL == kKS / 3, "");
   static constexpr int kBufs = kQL ? 3 : 4;      // tile buffers: one being read, the others in flight
   static constexpr int kQB = kWaves * kQL * 1024;
   static constexpr int kLds = kBufs * kTileB + kQB;
@@ -134,14 +71,14 @@ struct Attend {
 template <typename E, int DC, int DR, int WM, int WN>
 __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, AttendWs ws, float c2, uint32_t flip) {
   using C = Attend<DC, DR, WM, WN>;
-  constexpr int kNB = C::kNB, kBufs = C::kBufs, kPanels = C::kPanels;
+  constexpr int kNB = C::kNB, kBufs = C::kBufs, kPanels = C::kPanels, kAhead = 6;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLds];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN, l32 = lane & 31, hl = lane >> 5;
   // neighbours in the unit order share cache rows: keep them on one XCD (ids go round the 8 XCDs)
   const int w = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
   const WgDesc d = ws.wg[w];
-  int b = uniform(d.b), mt = uniform(d.mt), kt = uniform(d.kt), left = uniform(d.n);
+  int b = uniform(d.b), mt = uniform(d.mt), at = uniform(d.at), left = uniform(d.n);
   bool first = true;
   const uint8_t *cache = static_cast<const uint8_t *>(a.cache);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
@@ -166,30 +103,14 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
     const LatentSeq r = latent_seq(a, b);
     const LatentSeq s{uniform(r.t0), uniform(r.nq), uniform(r.len), uniform(r.before)};
     const int nt = row_tiles(a, s, C::kMT), kts = kv_tiles(s);
-    const int n = min(left, kts - kt);
-    if (nt > 0) {
-      // the wave's rows
+    const int units = min(left, kts + kOver - at);                       // of this row tile
+    const int kt = max(at - kOver, 0), n = max(at + units - kOver, 0) - kt;  // first cache tile, cache tiles
+    if (nt > 0 && n > 0) {
+      // the wave's rows; lanes behind the last row repeat it and store nothing
       const int row = mt * C::kMT + wm * 32 + l32;
       const bool live = row < s.nq * a.H;
-      const int qi = live ? row / a.H : 0, t = s.t0 + qi;
-      u16x8 q[C::kKS - C::kQL];
-      u16x8 *q_lds = reinterpret_cast<u16x8 *>(lds + kBufs * C::kTileB + wave * (C::kQL * 1024)) + lane;
-      {
-        const int h = live ? row - qi * a.H : 0;
-        const uint16_t *q1 = ws.q + ((int64_t)t * a.H + h) * DC + 8 * hl;
-        const uint16_t *q2 = static_cast<const uint16_t *>(a.q_rope) + t * a.rope_t + h * a.rope_h + 8 * hl;
-#pragma unroll
-        for (int k = 0; k < C::kKS; ++k) {
-          u32x4 v = {0, 0, 0, 0};
-          if (live) v = *reinterpret_cast<const u32x4 *>(16 * k < DC ? q1 + 16 * k : q2 + (16 * k - DC));
-          v ^= flip;
-          if (k < C::kQL)
-            q_lds[k * 64] = __builtin_bit_cast(u16x8, v);
-          else
-            q[k < C::kQL ? 0 : k - C::kQL] = __builtin_bit_cast(u16x8, v);
-        }
-      }
-      const uint64_t word = live && a.tree ? a.tree[t] : 0;
+      const int row_c = min(row, s.nq * a.H - 1), qi = row_c / a.H, t = s.t0 + qi;
+      const uint64_t word = a.tree ? a.tree[t] : 0;
       // the tokens of the tile from position j0 that the lane's row sees, as bits
       auto seen = [&](int j0) {
         const int old = min(max(s.before - j0, 0), 32), own = j0 - s.before;
@@ -202,62 +123,113 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
         return v & (uint32_t)((1ull << min(max(s.len - j0, 0), 32)) - 1);
       };
 
-      // The wave's 8 tokens of tile i of this run, into its buffer. Positions behind the sequence's last row repeat
-      // that row. Pages of 8 rows and more hold all 8: their id is a scalar load, which the count of outstanding
-      // vector loads does not see.
-      auto load = [&](int i) {
-        const int j0 = min((kt + i) * kNT + 8 * wave, (s.len - 1) & ~7);
-        const int r = min(ld_row, s.len - 1 - j0);
-        const uint32_t to = uniform(lds0 + (i % kBufs) * C::kTileB + wave * 1024);
-        if (a.page_shift >= 3) {
-          const int at = uniform(j0);
-          const int32_t *entry = a.page_table + (int64_t)b * a.max_pages + (at >> a.page_shift);
-          int page = uniform(*(const __attribute__((address_space(4))) int32_t *)(uintptr_t)entry);
-          if (page < 0 || page >= a.n_pages) {
-            if (lane == 0) atomicOr(a.err, (uint32_t)ERRF_LATENT);
-            page = 0;
-          }
-          const uint8_t *src =
-              uniform(cache + (((int64_t)page << a.page_shift) + (at & ((1 << a.page_shift) - 1))) * (C::kDK * 2));
-          const uint32_t off = r * (C::kDK * 2) + ld_unit * 16;
-#pragma unroll
-          for (int g = 0; g < kPanels; ++g)
-            lds_load16_s(uniform(src + g * 128), g == kPanels - 1 ? off + ld_last * 16 : off, to + g * C::kPanelB);
-        } else {
-          const uint8_t *src = cache + latent_row(a, b, j0 + r) * (C::kDK * 2) + ld_unit * 16;
-#pragma unroll
-          for (int g = 0; g < kPanels; ++g)
-            lds_load16_v(src + g * 128 + (g == kPanels - 1 ? ld_last * 16 : 0), to + g * C::kPanelB);
+      // The wave's 8 tokens of tile i of this run, into its buffer: prepared, then loaded panel by panel. Positions
+      // behind the sequence's last row repeat that row; behind the run's last tile nothing is loaded (but counted).
+      // Pages of 8 rows and more hold all 8 tokens: lane i then keeps the page of tile i of 64, so that a tile's page
+      // costs no memory access of its own.
+      auto first_of = [&](int i) { return min((kt + i) * kNT + 8 * wave, (s.len - 1) & ~7); };
+      int pages = 0;
+      auto read_pages = [&](int i) {
+        pages = a.page_table[(int64_t)b * a.max_pages + (first_of(i + lane) >> a.page_shift)];
+        if (pages < 0 || pages >= a.n_pages) {
+          atomicOr(a.err, (uint32_t)ERRF_LATENT);
+          pages = 0;
         }
       };
+      const uint8_t *src = nullptr;
+      uint32_t to = 0;
+      int on = 0;
+      auto prepare = [&](int i) {
+        const int j0 = uniform(first_of(i)), r = min(ld_row, s.len - 1 - j0);
+        if (a.page_shift >= 3) {
+          if ((i & 63) == 0) read_pages(i);
+          const int page = __builtin_amdgcn_readlane(pages, i & 63);
+          const int64_t row = ((int64_t)page << a.page_shift) + (j0 & ((1 << a.page_shift) - 1));
+          src = uniform(cache + row * (C::kDK * 2)) + (r * (C::kDK * 2) + ld_unit * 16);
+        } else {
+          src = cache + latent_row(a, b, j0 + r) * (C::kDK * 2) + ld_unit * 16;
+        }
+        to = uniform(lds0 + (i % kBufs) * C::kTileB + wave * 1024);
+        on = uniform(i < n ? -1 : 0);
+      };
+      auto load = [&](auto g) {
+        if constexpr (C::kDK % 64 && g == kPanels - 1)
+          lds_load16<g * 128>(src + ld_last * 16, to + g * C::kPanelB, on);
+        else
+          lds_load16<g * 128>(src, to + g * C::kPanelB, on);
+      };
+
+      // the first tiles' loads fly while the queries are read
+      if (s.len > 0)
+#pragma unroll
+        for (int i = 0; i < kBufs - 1; ++i) {
+          prepare(i);
+          static_for<0, kPanels>(load);
+        }
+      u16x8 q[C::kKS - C::kQL];
+      u16x8 *q_lds = reinterpret_cast<u16x8 *>(lds + kBufs * C::kTileB + wave * (C::kQL * 1024)) + lane;
+      {
+        const int h = row_c - qi * a.H;
+        const int64_t step = (int64_t)a.T * a.H * 16;
+        const uint16_t *q1 = ws.q + ((int64_t)s.t0 * a.H + row_c) * 16 + 8 * hl;
+        const uint16_t *q2 = static_cast<const uint16_t *>(a.q_rope) + t * a.rope_t + h * a.rope_h + 8 * hl;
+#pragma unroll
+        for (int k = 0; k < C::kKS; ++k) {
+          const u32x4 v = *reinterpret_cast<const u32x4 *>(16 * k < DC ? q1 + k * step : q2 + (16 * k - DC)) ^ flip;
+          if (C::in_lds(k))
+            q_lds[k / 3 * 64] = __builtin_bit_cast(u16x8, v);
+          else
+            q[C::kQL ? k - k / 3 : k] = __builtin_bit_cast(u16x8, v);
+        }
+      }
 
       AccTile<E> acc[kNB];
       clear(acc);
       float m = -__builtin_inff(), l = 0.0f;
-      if (s.len > 0) {
-#pragma unroll
-        for (int i = 0; i < kBufs - 1; ++i)
-          if (i < n) load(i);
+      if (s.len > 0)
         for (int it = 0; it < n; ++it) {
-          // the tile is complete when only the loads of later ones are outstanding
-          if (kBufs == 4 && it + 2 < n)
-            WAIT_VM(2 * kPanels);
-          else if (it + 1 < n)
-            WAIT_VM(kPanels);
-          else
-            WAIT_VM(0);
-          asm volatile("s_barrier" ::: "memory");  // for every wave's part of it; the oldest buffer's readers are done
-          if (it + kBufs - 1 < n) load(it + kBufs - 1);
+          WAIT_VM((kBufs - 2) * kPanels);  // only later tiles' loads are outstanding: the wave's part of this one is there
+          asm volatile("s_barrier" ::: "memory");  // the other waves' parts are; the oldest buffer's readers are done
+          prepare(it + kBufs - 1);
           uint8_t *kv = lds + (it % kBufs) * C::kTileB;
+          auto v_read = [&](int i) {  // block i % kNB of latents, tokens 16 (i / kNB) ..
+            const uint8_t *src = kv + ((wn * kNB + i % kNB) >> 1) * C::kPanelB + i / kNB * (16 * 128);
+            const u16x4 lo = lds_read_tr(src + v_off[0][i % kNB & 1]), hi = lds_read_tr(src + v_off[1][i % kNB & 1]);
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+          };
+          u16x8 ring[kAhead];
+          // Operands are read kAhead products before they are used, and the order is held: left to itself the
+          // compiler reads each one just before its product and waits for it.
           f32x16 z = {}, z1 = {};
+          {
+            auto k_read = [&](int k) {
+              return *reinterpret_cast<const u16x8 *>(kv + k_off[k & 3] + (k >> 2) * C::kPanelB);
+            };
+            u16x8 qf[2];
 #pragma unroll
-          for (int k = 0; k < C::kKS; ++k) {
-            const u16x8 kf = *reinterpret_cast<const u16x8 *>(kv + k_off[k & 3] + (k >> 2) * C::kPanelB);
-            const u16x8 qf = k < C::kQL ? q_lds[k * 64] : q[k < C::kQL ? 0 : k - C::kQL];
-            if (k & 1)
-              z1 = E::mfma(kf, qf, z1);
-            else
-              z = E::mfma(kf, qf, z);
+            for (int k = 0; k < kAhead; ++k) ring[k] = k_read(k);
+            if (C::kQL) {
+              qf[0] = q_lds[0];
+              qf[1] = q_lds[64];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            // The next tile's loads go in between: a wave that issued its 9 in a row would stand still until the
+            // memory path has taken them, 16 cycles each for 4 waves. The last steps read the second product's first
+            // operands.
+            static_for<0, C::kKS>([&](auto k) {
+              const u16x8 qk = C::in_lds(k) ? qf[k / 3 & 1] : q[C::kQL ? k - k / 3 : k];
+              if (k & 1)
+                z1 = E::mfma(ring[k % kAhead], qk, z1);
+              else
+                z = E::mfma(ring[k % kAhead], qk, z);
+              if (k + kAhead < C::kKS)
+                ring[k % kAhead] = k_read(k + kAhead);
+              else if (k + kAhead - C::kKS < 2 * kNB)
+                ring[k % kAhead] = v_read(k + kAhead - C::kKS);
+              if (C::in_lds(k) && k / 3 + 2 < C::kQL) qf[k / 3 & 1] = q_lds[(k / 3 + 2) * 64];
+              if constexpr (k % 4 == 1) load(std::integral_constant<int, k / 4>{});
+              __builtin_amdgcn_sched_barrier(0);
+            });
           }
           z += z1;
           const int j0 = (kt + it) * kNT;
@@ -295,12 +267,14 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
                 z[i] = (bad >> (8 * (i >> 2) + 4 * hl + (i & 3))) & 1 ? -__builtin_inff() : z[i];
               if (bad & (vis << (4 * hl))) l = __builtin_nanf("");
               __syncthreads();
+#pragma unroll
+              for (int i = 0; i < kAhead && i < 2 * kNB; ++i) ring[(C::kKS + i) % kAhead] = v_read(i);  // once more
             }
           }
           float top = z[0];
 #pragma unroll
           for (int i = 1; i < 16; ++i) top = fmaxf(top, z[i]);
-          top = fmaxf(top, __shfl_xor(top, 32, 64)) * c2;
+          top = max_halves(top) * c2;
           // The reference of the exponentials follows the maximum only when that has grown by 2^8: until then
           // weights up to 2^8 are as exact as weights up to 1, and the sums need no rescaling.
           if (__any(top > m + 8.0f)) {
@@ -312,27 +286,27 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
             for (int i = 0; i < kNB; ++i) acc[i].scale(f);
           }
           const float base = m == -__builtin_inff() ? 0.0f : -m;
-          u16x8 p[2];
+          // the second half's exponentials go between the first half's products
+          auto weight = [&](int i) {
+            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i], c2, base));
+            l += e;
+            return e;
+          };
+          f32x8 e;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            f32x8 e;
+          for (int i = 0; i < 8; ++i) e[i] = weight(i);
+          u16x8 p = E::from_f32x8(e);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[8 * half + i], c2, base));
-              l += e[i];
-            }
-            p[half] = E::from_f32x8(e);
+          for (int i = 0; i < 2 * kNB; ++i) {
+            if (i == kNB) p = E::from_f32x8(e);
+            acc[i % kNB].mfma(ring[(C::kKS + i) % kAhead], p);
+            if (i + kAhead < 2 * kNB) ring[(C::kKS + i) % kAhead] = v_read(i + kAhead);
+            if (i < kNB)
+#pragma unroll
+              for (int j = i * 8 / kNB; j < (i + 1) * 8 / kNB; ++j) e[j] = weight(8 + j);
+            __builtin_amdgcn_sched_barrier(0);
           }
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-            for (int nb = 0; nb < kNB; ++nb) {
-              const uint8_t *src = kv + ((wn * kNB + nb) >> 1) * C::kPanelB + ks * 16 * 128;
-              const u16x4 lo = lds_read_tr(src + v_off[0][nb & 1]), hi = lds_read_tr(src + v_off[1][nb & 1]);
-              acc[nb].mfma(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), p[ks]);
-            }
         }
-      }
       l += __shfl_xor(l, 32, 64);
       settle(acc);
       if (n == kts) {  // the whole row tile: finished here
@@ -361,8 +335,8 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
       __syncthreads();  // the tiles are no longer read
     }
     first = false;
-    left -= nt > 0 ? n : 0;
-    kt = 0;
+    left -= nt > 0 ? units : 0;
+    at = 0;
     if (nt == 0 || ++mt == nt) {
       mt = 0;
       ++b;
@@ -370,46 +344,73 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
   }
 }
 
-// Join of the row tiles that several workgroups share: a wave takes one block
-// of 32 latents of 32 rows.
+// Join of the row tiles that several workgroups share: a workgroup takes 8
+// latents (1 KB of each partial result) of 32 rows, its four waves every fourth
+// partial result each, and joins the waves through LDS.
 template <typename E, int WM>
 __global__ __launch_bounds__(256) void latent_merge_kernel(LatentArgs a, AttendWs ws) {
+  __shared__ float box[4][64][8];
   const int ti = blockIdx.x / WM, wm = blockIdx.x % WM;
   if (ti >= ws.head->n_tiles) return;
   const TileDesc d = ws.tile[ti];
   if (d.w0 == d.w1) return;
-  const int lane = threadIdx.x & 63, nb = blockIdx.y * 4 + (threadIdx.x >> 6), kNB = a.dc / 32;
-  const int l32 = lane & 31, hl = lane >> 5;
-  const LatentSeq s = latent_seq(a, d.b);
-  const int row = d.mt * 32 * WM + wm * 32 + l32;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), j = blockIdx.y, l32 = lane & 31, hl = lane >> 5;
   const int64_t per = ws.head->per;
+  const int64_t whole = (int64_t)a.dc * 32;  // floats of a partial result's 32 rows
   float m = -__builtin_inff(), l = 0.0f;
-  for (int w = d.w0; w <= d.w1; ++w) {
-    const int slot = 2 * w + (w * per >= d.u0 ? 0 : 1);
-    const float2 v = ws.ml[(int64_t)slot * 32 * WM + wm * 32 + l32];
-    const float mn = fmaxf(m, v.x);
-    l = l * (m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn)) + v.y * (v.x == mn ? 1.0f : __builtin_amdgcn_exp2f(v.x - mn));
+  f32x4 acc = {};
+  constexpr int kB = 4;  // partial results read at a time
+  for (int w = d.w0 + wave; w <= d.w1; w += 4 * kB) {
+    float2 ml[kB];
+    f32x4 v[kB];
+#pragma unroll
+    for (int i = 0; i < kB; ++i) {
+      const int wi = min(w + 4 * i, d.w1);
+      const int64_t slot = (2 * wi + (wi * per >= d.u0 ? 0 : 1)) * WM + wm;
+      ml[i] = ws.ml[slot * 32 + l32];
+      v[i] = *reinterpret_cast<const f32x4 *>(ws.part + slot * whole + (j * 64 + lane) * 4);
+      if (w + 4 * i > d.w1) ml[i] = make_float2(-__builtin_inff(), 0.0f);
+    }
+    float mn = m;
+#pragma unroll
+    for (int i = 0; i < kB; ++i) mn = fmaxf(mn, ml[i].x);
+    const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+    l *= f;
+    acc *= f;
+#pragma unroll
+    for (int i = 0; i < kB; ++i) {
+      const float g = w + 4 * i > d.w1 ? 0.0f : ml[i].x == mn ? 1.0f : __builtin_amdgcn_exp2f(ml[i].x - mn);
+      l += ml[i].y * g;
+      acc += v[i] * g;
+    }
     m = mn;
   }
-  f32x4 acc[4] = {};
-  for (int w = d.w0; w <= d.w1; ++w) {
-    const int slot = 2 * w + (w * per >= d.u0 ? 0 : 1);
-    const float mw = ws.ml[(int64_t)slot * 32 * WM + wm * 32 + l32].x;
-    const float f = mw == m ? 1.0f : __builtin_amdgcn_exp2f(mw - m);
-    const float *o = ws.part + ((int64_t)slot * WM + wm) * (kNB * 1024) + (nb * 4 * 64 + lane) * 4;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] += *reinterpret_cast<const f32x4 *>(o + j * 256) * f;
-  }
+  float *mine = box[wave][lane];
+  *reinterpret_cast<f32x4 *>(mine) = acc;
+  mine[4] = m;
+  mine[5] = l;
+  __syncthreads();
+  if (wave) return;
+  const LatentSeq s = latent_seq(a, d.b);
+  const int row = d.mt * 32 * WM + wm * 32 + l32;
   if (row >= s.nq * a.H) return;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t *o = ws.u + ((int64_t)s.t0 * a.H + row) * a.dc + 32 * nb + 4 * hl;
+  float mx = m;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    u16x4 v;
+  for (int w = 1; w < 4; ++w) mx = fmaxf(mx, box[w][lane][4]);
+  f32x4 sum = {};
+  float ls = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = E::from_f32(acc[j][e] * inv);
-    *reinterpret_cast<u16x4 *>(o + 8 * j) = v;
+  for (int w = 0; w < 4; ++w) {
+    const float *o = box[w][lane];
+    const float f = o[4] == mx ? 1.0f : __builtin_amdgcn_exp2f(o[4] - mx);
+    sum += *reinterpret_cast<const f32x4 *>(o) * f;
+    ls += o[5] * f;
   }
+  const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+  u16x4 v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = E::from_f32(sum[e] * inv);
+  *reinterpret_cast<u16x4 *>(ws.u + ((int64_t)s.t0 * a.H + row) * a.dc + 8 * j + 4 * hl) = v;
 }
 
 template <typename E, int DC, int DR, int WM, int WN>
@@ -427,27 +428,28 @@ moe_status launch(moe_ctx *ctx, const LatentArgs &a) {
   moe_status st = moe_scratch(ctx, lay.size, &scr);
   if (st) return st;
   char *p = static_cast<char *>(scr);
-  const AttendWs ws{reinterpret_cast<PlanHead *>(p + o_head), reinterpret_cast<WgDesc *>(p + o_wg),
-                    reinterpret_cast<TileDesc *>(p + o_tile), reinterpret_cast<float *>(p + o_part),
-                    reinterpret_cast<float2 *>(p + o_ml),     reinterpret_cast<uint16_t *>(p + o_q),
-                    reinterpret_cast<uint16_t *>(p + o_u)};
-  hipLaunchKernelGGL(latent_plan_kernel, dim3(1), dim3(1024), 0, ctx->stream, a, ws, C::kMT, n_wg, 1);
-  MOE_CHECK_LAUNCH("latent_plan_kernel");
-  const int64_t hc = (int64_t)a.H * DC;
-  const HeadGemm absorb{static_cast<const uint16_t *>(a.q_nope), static_cast<const uint16_t *>(a.w_kt), ws.q, nullptr,
-                        nullptr, nullptr, a.T, DC, a.dn, a.nope_t, a.nope_h, (int64_t)DC * a.dn, hc, DC};
-  if ((st = launch_head_gemm(ctx, E::kDtype, absorb, a.H))) return st;
+  PlanHead *head = reinterpret_cast<PlanHead *>(p + o_head);
+  WgDesc *wg = reinterpret_cast<WgDesc *>(p + o_wg);
+  TileDesc *tile = reinterpret_cast<TileDesc *>(p + o_tile);
+  uint16_t *q = reinterpret_cast<uint16_t *>(p + o_q), *u = reinterpret_cast<uint16_t *>(p + o_u);
+  const AttendWs ws{head, wg, tile, reinterpret_cast<float *>(p + o_part), reinterpret_cast<float2 *>(p + o_ml), q, u};
+  const int64_t hc = (int64_t)a.H * DC, rows16 = (int64_t)a.T * a.H * 16;
+  const HeadGemm absorb{static_cast<const uint16_t *>(a.q_nope), static_cast<const uint16_t *>(a.w_kt), q, nullptr,
+                        nullptr, nullptr, a.T, DC, a.dn, a.nope_t, a.nope_h, (int64_t)DC * a.dn,
+                        (int64_t)a.H * 16, 16, rows16};
+  const LatentPlan plan{a, head, wg, tile, C::kMT, kNT, kOver, n_wg};
+  if ((st = launch_head_gemm(ctx, E::kDtype, absorb, a.H, plan))) return st;
   const float c2 = latent_c2(a.scale);
   hipLaunchKernelGGL((latent_attend_kernel<E, DC, DR, WM, WN>), dim3(n_wg), dim3(256), 0, ctx->stream, a, ws,
                      c2, a.scale < 0 ? 0x80008000u : 0u);
   MOE_CHECK_LAUNCH("latent_attend_kernel");
-  hipLaunchKernelGGL((latent_merge_kernel<E, WM>), dim3((unsigned)(tiles * WM), DC / 128), dim3(256), 0, ctx->stream,
+  hipLaunchKernelGGL((latent_merge_kernel<E, WM>), dim3((unsigned)(tiles * WM), DC / 8), dim3(256), 0, ctx->stream,
                      a, ws);
   MOE_CHECK_LAUNCH("latent_merge_kernel");
-  const HeadGemm up{ws.u, static_cast<const uint16_t *>(a.w_kv) + (int64_t)a.dn * DC, static_cast<uint16_t *>(a.out),
+  const HeadGemm up{u, static_cast<const uint16_t *>(a.w_kv) + (int64_t)a.dn * DC, static_cast<uint16_t *>(a.out),
                     nullptr, a.q_start, a.q_start + a.B, a.T, a.dv, DC, hc, DC, (int64_t)(a.dn + a.dv) * DC,
-                    (int64_t)a.H * a.dv, a.dv};
-  return launch_head_gemm(ctx, E::kDtype, up, a.H);
+                    (int64_t)a.H * a.dv, a.dv, 16};
+  return launch_head_gemm(ctx, E::kDtype, up, a.H, LatentPlan{});
 }
 
 template <typename E, int DC, int DR>

@@ -230,7 +230,7 @@ __global__ __launch_bounds__(512, 1) void latent_prompt_kernel(LatentArgs a, Pro
     for (int tb = 0; tb < kTB; ++tb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, z[tb][i]);
-    top = fmaxf(top, __shfl_xor(top, 32, 64)) * c2;
+    top = max_halves(top) * c2;
     // the reference follows the maximum when that has grown by 2^8 (see latent_attend.hip)
     if (__any(top > m + 8.0f)) {
       const float mn = fmaxf(m, top);
@@ -301,8 +301,8 @@ moe_status launch(moe_ctx *ctx, const LatentArgs &a, int64_t n_kv) {
     MOE_CHECK_LAUNCH("prompt_rows_kernel");
     const HeadGemm expand{static_cast<const uint16_t *>(a.cache), static_cast<const uint16_t *>(a.w_kv), ws.x, ws.rows,
                           nullptr, ws.off + a.B, (int)n_kv, DN + DV, a.dc, a.dc + DR, 0, (int64_t)(DN + DV) * a.dc,
-                          DN + DV, n_kv * (DN + DV)};
-    if ((st = launch_head_gemm(ctx, E::kDtype, expand, a.H))) return st;
+                          DN + DV, n_kv * (DN + DV), 16};
+    if ((st = launch_head_gemm(ctx, E::kDtype, expand, a.H, LatentPlan{}))) return st;
   }
   const float c2 = latent_c2(a.scale);
   hipLaunchKernelGGL((latent_prompt_kernel<E, DN, DR, DV>), dim3((unsigned)(tiles * ((a.H + 7) / 8) * 8)), dim3(512), 0,

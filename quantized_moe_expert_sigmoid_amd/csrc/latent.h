@@ -48,34 +48,44 @@ struct WgDesc {
   int b, mt, at, n;  // first unit: sequence, row tile, place in the row tile's units; number of units
 };
 struct TileDesc {
-  int b, mt, w0, w1;  // row tile; the workgroups that share its cache tiles
+  int b, mt, w0, w1;  // a row tile whose cache tiles several workgroups share, and those
   int64_t u0;         // its first unit
 };
 struct PlanHead {
-  int64_t per;  // units of a workgroup
-  int n_tiles;
+  int64_t per;   // units of a workgroup
+  int over;      // units a row tile has ahead of its cache tiles
+  int n_shared;  // TileDescs
 };
 struct LatentPlan {
   LatentArgs a;
   PlanHead *head;
   WgDesc *wg;
-  TileDesc *tile;
-  int rows, tokens, over;  // rows of a row tile, tokens of a cache tile, units charged for starting a row tile
+  TileDesc *shared;
+  int rows, tokens, over;  // rows of a row tile, tokens of a cache tile, units charged for a row tile's start and end
   int n_wg;                // 0: no plan
 };
 
 // C[m][h][n] = sum_k A[m][h][k] B[h][n][k]; element (m, h, 0) of A at m a_m + h
-// a_h, (m, h, n) of C at m c_m + h c_h + n / 16 c_n + n % 16; B's heads b_h
-// apart. K is a multiple of 64, N of 32.
+// a_h, of C at m c_m + h c_h; B's heads b_h apart. K is a multiple of 64, N of
+// 64.
 struct HeadGemm {
   const uint16_t *A, *B;
   uint16_t *C;
-  const int64_t *rows;      // nullable: A's row of m
-  const int32_t *lo, *hi;   // nullable, on the device: only rows lo <= m < hi
+  const int32_t *lo, *hi;  // nullable, on the device: only rows lo <= m < hi
   int M, N, K;
-  int64_t a_m, a_h, b_h, c_m, c_h, c_n;
+  int64_t a_m, a_h, b_h, c_m, c_h;
 };
 moe_status launch_head_gemm(moe_ctx *ctx, int dtype, const HeadGemm &g, int H, const LatentPlan &plan);
+
+// All heads' keys and values of the rows m < *hi (<= M): C[h][m][n] = sum_k
+// A[m][k] B[h][n][k], N a multiple of 64, K of 128.
+struct ExpandGemm {
+  const uint16_t *A, *B;
+  uint16_t *C;
+  const int32_t *hi;
+  int M, H, N, K;
+};
+moe_status launch_expand_gemm(moe_ctx *ctx, int dtype, const ExpandGemm &g);
 
 // The exponentials are powers of two of c2 z. A negative scale turns the
 // queries' signs instead, and zero is taken as 1e-30 (masked scores, -inf, must
@@ -202,6 +212,18 @@ __device__ void settle(AccTile<E> (&t)[N]);
 template <typename E, int N>
 __device__ void clear(AccTile<E> (&t)[N]);
 #endif
+
+// Results of a 32 x 32 product, four consecutive rows a lane, as elements: the
+// 16 rows 16 j .. of a lane's column, of which lane l stores 8, rows 16 j + 8 (l /
+// 32) .., in one 16-byte store.
+template <typename E>
+__device__ __forceinline__ u32x4 rows8(f32x4 a, f32x4 b) {  // rows 16 j + 4 half .., rows 16 j + 8 + 4 half ..
+  const f32x8 f = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  const u32x4 p = __builtin_bit_cast(u32x4, E::from_f32x8(f));
+  const auto x = __builtin_amdgcn_permlane32_swap(p[0], p[2], false, false);
+  const auto y = __builtin_amdgcn_permlane32_swap(p[1], p[3], false, false);
+  return u32x4{x[0], y[0], x[1], y[1]};
+}
 
 // Maximum of lanes l and l + 32, in both.
 __device__ __forceinline__ float max_halves(float v) {

@@ -23,19 +23,19 @@ constexpr int kNT = 32;  // tokens of a cache tile
 
 // A unit of work is one cache tile for one row tile. Units are numbered sequence
 // by sequence, row tile by row tile, cache tile by cache tile, each row tile
-// with kOver units ahead of its cache tiles for what starting and ending it
-// costs; workgroup w takes units [w per, (w + 1) per), so that all have about
+// with up to kOver units ahead of its cache tiles for what starting and ending
+// it costs; workgroup w takes units [w per, (w + 1) per), so that all have about
 // the same work whatever the lengths are. A row tile whose cache tiles several
 // workgroups share is joined from their partial results by the merge kernel.
-constexpr int kOver = 2;
+constexpr int kOver = 6;
 
 struct AttendWs {
   const PlanHead *head;
   const WgDesc *wg;
-  const TileDesc *tile;
+  const TileDesc *shared;
   float *part;        // [2 n_wg][WM][dc / 32][4][64] x 4: O^T in the order of the lanes' registers
   float2 *ml;         // [2 n_wg][32 WM]: running maximum and sum
-  const uint16_t *q;  // [dc / 16][T][H][16] absorbed queries: 32 rows' operand of a step is 1 KB in a row
+  const uint16_t *q;  // [T][H][dc] absorbed queries
   uint16_t *u;        // [T][H][dc] sums of latents
 };
 
@@ -72,12 +72,14 @@ template <typename E, int DC, int DR, int WM, int WN>
 __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, AttendWs ws, float c2, uint32_t flip) {
   using C = Attend<DC, DR, WM, WN>;
   constexpr int kNB = C::kNB, kBufs = C::kBufs, kPanels = C::kPanels, kAhead = 6;
+  constexpr int kLoadStep = (C::kKS - 4) / kPanels;  // a panel's load every so many products
   __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLds];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN, l32 = lane & 31, hl = lane >> 5;
   // neighbours in the unit order share cache rows: keep them on one XCD (ids go round the 8 XCDs)
   const int w = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
   const WgDesc d = ws.wg[w];
+  const int over = uniform(ws.head->over);
   int b = uniform(d.b), mt = uniform(d.mt), at = uniform(d.at), left = uniform(d.n);
   bool first = true;
   const uint8_t *cache = static_cast<const uint8_t *>(a.cache);
@@ -103,8 +105,8 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
     const LatentSeq r = latent_seq(a, b);
     const LatentSeq s{uniform(r.t0), uniform(r.nq), uniform(r.len), uniform(r.before)};
     const int nt = row_tiles(a, s, C::kMT), kts = kv_tiles(s);
-    const int units = min(left, kts + kOver - at);                       // of this row tile
-    const int kt = max(at - kOver, 0), n = max(at + units - kOver, 0) - kt;  // first cache tile, cache tiles
+    const int units = min(left, kts + over - at);                        // of this row tile
+    const int kt = max(at - over, 0), n = max(at + units - over, 0) - kt;  // first cache tile, cache tiles
     if (nt > 0 && n > 0) {
       // the wave's rows; lanes behind the last row repeat it and store nothing
       const int row = mt * C::kMT + wm * 32 + l32;
@@ -138,44 +140,52 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
       };
       const uint8_t *src = nullptr;
       uint32_t to = 0;
-      int on = 0;
-      auto prepare = [&](int i) {
-        const int j0 = uniform(first_of(i)), r = min(ld_row, s.len - 1 - j0);
-        if (a.page_shift >= 3) {
-          if ((i & 63) == 0) read_pages(i);
-          const int page = __builtin_amdgcn_readlane(pages, i & 63);
-          const int64_t row = ((int64_t)page << a.page_shift) + (j0 & ((1 << a.page_shift) - 1));
-          src = uniform(cache + row * (C::kDK * 2)) + (r * (C::kDK * 2) + ld_unit * 16);
+      int on = 0, j0_next = 0, r_next = 0;
+      int64_t row_next = 0;
+      auto prepare = [&](int i, auto part) {  // in four parts, for between the products
+        if constexpr (part == 0) {
+          j0_next = uniform(first_of(i));
+          r_next = min(ld_row, s.len - 1 - j0_next);
+          on = uniform(i < n ? -1 : 0);
+        } else if constexpr (part == 1) {
+          if (a.page_shift >= 3) {
+            if ((i & 63) == 0) read_pages(i);
+            const int page = __builtin_amdgcn_readlane(pages, i & 63);
+            row_next = ((int64_t)page << a.page_shift) + (j0_next & ((1 << a.page_shift) - 1));
+          } else {
+            row_next = latent_row(a, b, j0_next + r_next);
+            r_next = 0;
+          }
+        } else if constexpr (part == 2) {
+          to = uniform(lds0 + (i % kBufs) * C::kTileB + wave * 1024);
+          src = cache + row_next * (C::kDK * 2);
         } else {
-          src = cache + latent_row(a, b, j0 + r) * (C::kDK * 2) + ld_unit * 16;
+          src += r_next * (C::kDK * 2) + ld_unit * 16;
         }
-        to = uniform(lds0 + (i % kBufs) * C::kTileB + wave * 1024);
-        on = uniform(i < n ? -1 : 0);
       };
       auto load = [&](auto g) {
         if constexpr (C::kDK % 64 && g == kPanels - 1)
-          lds_load16<g * 128>(src + ld_last * 16, to + g * C::kPanelB, on);
+          lds_load16<g * 128>(src + ld_last * 16, uniform(to + g * C::kPanelB), uniform(on));
         else
-          lds_load16<g * 128>(src, to + g * C::kPanelB, on);
+          lds_load16<g * 128>(src, uniform(to + g * C::kPanelB), uniform(on));
       };
 
       // the first tiles' loads fly while the queries are read
       if (s.len > 0)
 #pragma unroll
         for (int i = 0; i < kBufs - 1; ++i) {
-          prepare(i);
+          static_for<0, 4>([&](auto part) { prepare(i, part); });
           static_for<0, kPanels>(load);
         }
       u16x8 q[C::kKS - C::kQL];
       u16x8 *q_lds = reinterpret_cast<u16x8 *>(lds + kBufs * C::kTileB + wave * (C::kQL * 1024)) + lane;
       {
         const int h = row_c - qi * a.H;
-        const int64_t step = (int64_t)a.T * a.H * 16;
-        const uint16_t *q1 = ws.q + ((int64_t)s.t0 * a.H + row_c) * 16 + 8 * hl;
+        const uint16_t *q1 = ws.q + ((int64_t)s.t0 * a.H + row_c) * DC + 8 * hl;
         const uint16_t *q2 = static_cast<const uint16_t *>(a.q_rope) + t * a.rope_t + h * a.rope_h + 8 * hl;
 #pragma unroll
         for (int k = 0; k < C::kKS; ++k) {
-          const u32x4 v = *reinterpret_cast<const u32x4 *>(16 * k < DC ? q1 + k * step : q2 + (16 * k - DC)) ^ flip;
+          const u32x4 v = *reinterpret_cast<const u32x4 *>(16 * k < DC ? q1 + 16 * k : q2 + (16 * k - DC)) ^ flip;
           if (C::in_lds(k))
             q_lds[k / 3 * 64] = __builtin_bit_cast(u16x8, v);
           else
@@ -190,7 +200,6 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
         for (int it = 0; it < n; ++it) {
           WAIT_VM((kBufs - 2) * kPanels);  // only later tiles' loads are outstanding: the wave's part of this one is there
           asm volatile("s_barrier" ::: "memory");  // the other waves' parts are; the oldest buffer's readers are done
-          prepare(it + kBufs - 1);
           uint8_t *kv = lds + (it % kBufs) * C::kTileB;
           auto v_read = [&](int i) {  // block i % kNB of latents, tokens 16 (i / kNB) ..
             const uint8_t *src = kv + ((wn * kNB + i % kNB) >> 1) * C::kPanelB + i / kNB * (16 * 128);
@@ -227,7 +236,10 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
               else if (k + kAhead - C::kKS < 2 * kNB)
                 ring[k % kAhead] = v_read(k + kAhead - C::kKS);
               if (C::in_lds(k) && k / 3 + 2 < C::kQL) qf[k / 3 & 1] = q_lds[(k / 3 + 2) * 64];
-              if constexpr (k % 4 == 1) load(std::integral_constant<int, k / 4>{});
+              if constexpr (k < 4)
+                prepare(it + kBufs - 1, k);
+              else if constexpr ((k - 4) % kLoadStep == 0 && (k - 4) / kLoadStep < kPanels)
+                load(std::integral_constant<int, (k - 4) / kLoadStep>{});
               __builtin_amdgcn_sched_barrier(0);
             });
           }
@@ -311,17 +323,14 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
       settle(acc);
       if (n == kts) {  // the whole row tile: finished here
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint16_t *o = ws.u + ((int64_t)s.t0 * a.H + row) * DC + wn * (kNB * 32) + 4 * hl;
-        if (live)
+        uint16_t *o = ws.u + ((int64_t)s.t0 * a.H + row) * DC + wn * (kNB * 32) + 8 * hl;
 #pragma unroll
-          for (int i = 0; i < kNB; ++i)
+        for (int i = 0; i < kNB; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              u16x4 v;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] = E::from_f32(acc[i].get(4 * j + e) * inv);
-              *reinterpret_cast<u16x4 *>(o + 32 * i + 8 * j) = v;
-            }
+          for (int j = 0; j < 4; j += 2) {
+            const u32x4 v = rows8<E>(acc[i].get4(j) * inv, acc[i].get4(j + 1) * inv);
+            if (live) *reinterpret_cast<u32x4 *>(o + 32 * i + 8 * j) = v;
+          }
       } else {
         const int slot = 2 * w + (first ? 0 : 1);
         float *o = ws.part + (((int64_t)slot * WM + wm) * WN + wn) * (kNB * 1024);
@@ -344,83 +353,130 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
   }
 }
 
-// Join of the row tiles that several workgroups share: a workgroup takes 8
-// latents (1 KB of each partial result) of 32 rows, its four waves every fourth
-// partial result each, and joins the waves through LDS.
-template <typename E, int WM>
+// Join of the row tiles that several workgroups share: a workgroup takes 8 J
+// latents (J runs of 1 KB of each partial result) of 32 rows. J = 8, up to kFew
+// partial results: a wave takes two of the runs. Otherwise a wave takes every
+// fourth partial result, and the waves are joined through LDS. J = 1 is for few
+// row tiles of many partial results, J = 8 for many row tiles (one token over
+// 131072 rows: 17 us with 1, 66 us with 8; 64 tokens over 1000-8000 rows: 26 and
+// 20 us).
+constexpr int kFew = 16;
+
+template <typename E, int WM, int J>
 __global__ __launch_bounds__(256) void latent_merge_kernel(LatentArgs a, AttendWs ws) {
-  __shared__ float box[4][64][8];
+  __shared__ float box[4][J][64][4];
+  __shared__ float2 box_ml[4][64];
   const int ti = blockIdx.x / WM, wm = blockIdx.x % WM;
-  if (ti >= ws.head->n_tiles) return;
-  const TileDesc d = ws.tile[ti];
-  if (d.w0 == d.w1) return;
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), j = blockIdx.y, l32 = lane & 31, hl = lane >> 5;
-  const int64_t per = ws.head->per;
-  const int64_t whole = (int64_t)a.dc * 32;  // floats of a partial result's 32 rows
-  float m = -__builtin_inff(), l = 0.0f;
-  f32x4 acc = {};
-  constexpr int kB = 4;  // partial results read at a time
-  for (int w = d.w0 + wave; w <= d.w1; w += 4 * kB) {
-    float2 ml[kB];
-    f32x4 v[kB];
+  if (ti >= ws.head->n_shared) return;
+  const TileDesc d = ws.shared[ti];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), l32 = lane & 31, hl = lane >> 5;
+  const int64_t per = ws.head->per, whole = (int64_t)a.dc * 32;  // floats of a partial result's 32 rows
+  const int j0 = blockIdx.y * J, n = d.w1 - d.w0 + 1;
+  auto slot = [&](int i) {
+    const int w = d.w0 + min(i, n - 1);
+    return (int64_t)(2 * w + (w * per >= d.u0 ? 0 : 1)) * WM + wm;
+  };
+  auto pow2 = [](float x, float top) { return x == top ? 1.0f : __builtin_amdgcn_exp2f(x - top); };
+  auto store = [&](int j, f32x4 sum, float l) {
+    const LatentSeq s = latent_seq(a, d.b);
+    const int row = d.mt * 32 * WM + wm * 32 + l32;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    u16x4 v;
 #pragma unroll
-    for (int i = 0; i < kB; ++i) {
-      const int wi = min(w + 4 * i, d.w1);
-      const int64_t slot = (2 * wi + (wi * per >= d.u0 ? 0 : 1)) * WM + wm;
-      ml[i] = ws.ml[slot * 32 + l32];
-      v[i] = *reinterpret_cast<const f32x4 *>(ws.part + slot * whole + (j * 64 + lane) * 4);
-      if (w + 4 * i > d.w1) ml[i] = make_float2(-__builtin_inff(), 0.0f);
+    for (int e = 0; e < 4; ++e) v[e] = E::from_f32(sum[e] * inv);
+    if (row < s.nq * a.H)
+      *reinterpret_cast<u16x4 *>(ws.u + ((int64_t)s.t0 * a.H + row) * a.dc + 8 * (j0 + j) + 4 * hl) = v;
+  };
+  if (J == 8 && n <= kFew) {
+    float2 ml[kFew];
+    float m = -__builtin_inff(), l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kFew; ++i)
+      if (i < n) ml[i] = ws.ml[slot(i) * 32 + l32];
+    f32x4 v[2][4], sum[2] = {};
+#pragma unroll
+    for (int i = 0; i < kFew; ++i)
+      if (i < n) m = fmaxf(m, ml[i].x);
+#pragma unroll
+    for (int i0 = 0; i0 < kFew; i0 += 4) {
+      if (i0 >= n) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          v[j][i] = *reinterpret_cast<const f32x4 *>(ws.part + slot(i0 + i) * whole + ((j0 + 2 * wave + j) * 64 + lane) * 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i0 + i < n) {
+          const float f = pow2(ml[i0 + i].x, m);
+          l += ml[i0 + i].y * f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) sum[j] += v[j][i] * f;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) store(2 * wave + j, sum[j], l);
+    return;
+  }
+  float m = -__builtin_inff(), l = 0.0f;
+  f32x4 acc[J] = {};
+  constexpr int kB = 8 / J == 8 ? 4 : 1;  // partial results read at a time
+  for (int i = wave; i < n; i += 4 * kB) {
+    float2 ml[kB];
+    f32x4 v[kB][J];
+#pragma unroll
+    for (int k = 0; k < kB; ++k) {
+      ml[k] = ws.ml[slot(i + 4 * k) * 32 + l32];
+      const float *o = ws.part + slot(i + 4 * k) * whole + (j0 * 64 + lane) * 4;
+#pragma unroll
+      for (int j = 0; j < J; ++j) v[k][j] = *reinterpret_cast<const f32x4 *>(o + j * 256);
     }
     float mn = m;
 #pragma unroll
-    for (int i = 0; i < kB; ++i) mn = fmaxf(mn, ml[i].x);
-    const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+    for (int k = 0; k < kB; ++k) mn = i + 4 * k < n ? fmaxf(mn, ml[k].x) : mn;
+    const float f = pow2(m, mn);
     l *= f;
-    acc *= f;
 #pragma unroll
-    for (int i = 0; i < kB; ++i) {
-      const float g = w + 4 * i > d.w1 ? 0.0f : ml[i].x == mn ? 1.0f : __builtin_amdgcn_exp2f(ml[i].x - mn);
-      l += ml[i].y * g;
-      acc += v[i] * g;
-    }
+    for (int j = 0; j < J; ++j) acc[j] *= f;
+#pragma unroll
+    for (int k = 0; k < kB; ++k)
+      if (i + 4 * k < n) {
+        const float g = pow2(ml[k].x, mn);
+        l += ml[k].y * g;
+#pragma unroll
+        for (int j = 0; j < J; ++j) acc[j] += v[k][j] * g;
+      }
     m = mn;
   }
-  float *mine = box[wave][lane];
-  *reinterpret_cast<f32x4 *>(mine) = acc;
-  mine[4] = m;
-  mine[5] = l;
-  __syncthreads();
-  if (wave) return;
-  const LatentSeq s = latent_seq(a, d.b);
-  const int row = d.mt * 32 * WM + wm * 32 + l32;
-  if (row >= s.nq * a.H) return;
-  float mx = m;
 #pragma unroll
-  for (int w = 1; w < 4; ++w) mx = fmaxf(mx, box[w][lane][4]);
-  f32x4 sum = {};
-  float ls = 0.0f;
+  for (int j = 0; j < J; ++j) *reinterpret_cast<f32x4 *>(box[wave][j][lane]) = acc[j];
+  box_ml[wave][lane] = make_float2(m, l);
+  __syncthreads();
+  if (J == 1 && wave) return;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) m = fmaxf(m, box_ml[w][lane].x);
+  l = 0.0f;
+  constexpr int kJ = J == 1 ? 1 : J / 4;  // runs a wave finishes
+  f32x4 sum[kJ] = {};
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    const float *o = box[w][lane];
-    const float f = o[4] == mx ? 1.0f : __builtin_amdgcn_exp2f(o[4] - mx);
-    sum += *reinterpret_cast<const f32x4 *>(o) * f;
-    ls += o[5] * f;
-  }
-  const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-  u16x4 v;
+    const float2 ml = box_ml[w][lane];
+    const float f = pow2(ml.x, m);
+    l += ml.y * f;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = E::from_f32(sum[e] * inv);
-  *reinterpret_cast<u16x4 *>(ws.u + ((int64_t)s.t0 * a.H + row) * a.dc + 8 * j + 4 * hl) = v;
+    for (int j = 0; j < kJ; ++j) sum[j] += *reinterpret_cast<const f32x4 *>(box[w][kJ * wave + j][lane]) * f;
+  }
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) store(kJ * wave + j, sum[j], l);
 }
 
 template <typename E, int DC, int DR, int WM, int WN>
 moe_status launch(moe_ctx *ctx, const LatentArgs &a) {
   using C = Attend<DC, DR, WM, WN>;
   const int n_wg = ctx->n_cu / 8 * 8;  // a workgroup a CU: its buffers and accumulators fill one
-  const int64_t tiles = ((int64_t)a.T * a.H + C::kMT - 1) / C::kMT + a.B;
   MoeLayout lay;
   const size_t o_head = lay.take(sizeof(PlanHead)), o_wg = lay.take(sizeof(WgDesc) * n_wg),
-               o_tile = lay.take(sizeof(TileDesc) * tiles),
+               o_shared = lay.take(sizeof(TileDesc) * n_wg),
                o_part = lay.take(sizeof(float) * 2 * n_wg * C::kMT * DC),
                o_ml = lay.take(sizeof(float2) * 2 * n_wg * C::kMT),
                o_q = lay.take(2 * (size_t)a.T * a.H * DC), o_u = lay.take(2 * (size_t)a.T * a.H * DC);
@@ -430,25 +486,29 @@ moe_status launch(moe_ctx *ctx, const LatentArgs &a) {
   char *p = static_cast<char *>(scr);
   PlanHead *head = reinterpret_cast<PlanHead *>(p + o_head);
   WgDesc *wg = reinterpret_cast<WgDesc *>(p + o_wg);
-  TileDesc *tile = reinterpret_cast<TileDesc *>(p + o_tile);
+  TileDesc *shared = reinterpret_cast<TileDesc *>(p + o_shared);
   uint16_t *q = reinterpret_cast<uint16_t *>(p + o_q), *u = reinterpret_cast<uint16_t *>(p + o_u);
-  const AttendWs ws{head, wg, tile, reinterpret_cast<float *>(p + o_part), reinterpret_cast<float2 *>(p + o_ml), q, u};
-  const int64_t hc = (int64_t)a.H * DC, rows16 = (int64_t)a.T * a.H * 16;
+  const AttendWs ws{head, wg, shared, reinterpret_cast<float *>(p + o_part), reinterpret_cast<float2 *>(p + o_ml), q, u};
+  const int64_t hc = (int64_t)a.H * DC;
   const HeadGemm absorb{static_cast<const uint16_t *>(a.q_nope), static_cast<const uint16_t *>(a.w_kt), q, nullptr,
-                        nullptr, nullptr, a.T, DC, a.dn, a.nope_t, a.nope_h, (int64_t)DC * a.dn,
-                        (int64_t)a.H * 16, 16, rows16};
-  const LatentPlan plan{a, head, wg, tile, C::kMT, kNT, kOver, n_wg};
+                        nullptr, a.T, DC, a.dn, a.nope_t, a.nope_h, (int64_t)DC * a.dn, hc, DC};
+  const LatentPlan plan{a, head, wg, shared, C::kMT, kNT, kOver, n_wg};
   if ((st = launch_head_gemm(ctx, E::kDtype, absorb, a.H, plan))) return st;
   const float c2 = latent_c2(a.scale);
   hipLaunchKernelGGL((latent_attend_kernel<E, DC, DR, WM, WN>), dim3(n_wg), dim3(256), 0, ctx->stream, a, ws,
                      c2, a.scale < 0 ? 0x80008000u : 0u);
   MOE_CHECK_LAUNCH("latent_attend_kernel");
-  hipLaunchKernelGGL((latent_merge_kernel<E, WM>), dim3((unsigned)(tiles * WM), DC / 8), dim3(256), 0, ctx->stream,
-                     a, ws);
+  const int64_t tiles = ((int64_t)a.T * a.H + C::kMT - 1) / C::kMT;
+  if (tiles <= 16)
+    hipLaunchKernelGGL((latent_merge_kernel<E, WM, 1>), dim3((unsigned)std::min<int64_t>(n_wg, tiles + a.B) * WM, DC / 8),
+                       dim3(256), 0, ctx->stream, a, ws);
+  else
+    hipLaunchKernelGGL((latent_merge_kernel<E, WM, 8>), dim3((unsigned)std::min<int64_t>(n_wg, tiles + a.B) * WM, DC / 64),
+                       dim3(256), 0, ctx->stream, a, ws);
   MOE_CHECK_LAUNCH("latent_merge_kernel");
   const HeadGemm up{u, static_cast<const uint16_t *>(a.w_kv) + (int64_t)a.dn * DC, static_cast<uint16_t *>(a.out),
-                    nullptr, a.q_start, a.q_start + a.B, a.T, a.dv, DC, hc, DC, (int64_t)(a.dn + a.dv) * DC,
-                    (int64_t)a.H * a.dv, a.dv, 16};
+                    a.q_start, a.q_start + a.B, a.T, a.dv, DC, hc, DC, (int64_t)(a.dn + a.dv) * DC,
+                    (int64_t)a.H * a.dv, a.dv};
   return launch_head_gemm(ctx, E::kDtype, up, a.H, LatentPlan{});
 }
 

@@ -9,12 +9,14 @@
 // flight.
 #include "latent.h"
 
+#include <algorithm>
+
 namespace {
 
 constexpr int kRows = 256;  // query tokens of a workgroup
 
 // The plan: off[b] = first expanded row of sequence b (B + 1 entries), the
-// row tiles, the expanded rows' cache rows. Sequences that do not fit n_kv rows are
+// row tiles. Sequences that do not fit n_kv rows are
 // reported and left out (off = -1).
 struct PromptTile {
   int b, i0;
@@ -23,7 +25,7 @@ struct PromptWs {
   int32_t *off;      // [B + 1]
   int32_t *n_tiles;
   PromptTile *tile;
-  int64_t *rows;     // [n_kv] cache row of an expanded row
+  uint16_t *c;       // [n_kv][dc] latents
   uint16_t *kr;      // [n_kv][dr] rotary keys
   uint16_t *x;       // [H][n_kv][dn + dv] keys and values
   int64_t n_kv;
@@ -56,18 +58,19 @@ __global__ __launch_bounds__(1024) void prompt_plan_kernel(LatentArgs a, PromptW
   if (b == 1023) *ws.n_tiles = tiles[b];
 }
 
-// Cache rows and rotary keys of the expanded rows.
+// The sequences' cache rows one after another: a wave a row, 16 bytes a lane
+// (the rotary part by the first lanes again).
 __global__ __launch_bounds__(256) void prompt_rows_kernel(LatentArgs a, PromptWs ws) {
-  const int b = blockIdx.y, off = ws.off[b];
+  const int b = blockIdx.y, off = ws.off[b], lane = threadIdx.x & 63;
   if (off < 0) return;
   const LatentSeq s = latent_seq(a, b);
-  const int units = a.dr / 8;
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < s.len * units; i += gridDim.x * 256) {
-    const int j = i / units, u = i - j * units;
-    const int64_t row = latent_row(a, b, j);
-    if (u == 0) ws.rows[off + j] = row;
-    reinterpret_cast<u32x4 *>(ws.kr)[(int64_t)(off + j) * units + u] = *reinterpret_cast<const u32x4 *>(
-        static_cast<const uint16_t *>(a.cache) + row * (a.dc + a.dr) + a.dc + 8 * u);
+  for (int j = blockIdx.x * 4 + (threadIdx.x >> 6); j < s.len; j += gridDim.x * 4) {
+    const uint16_t *row = static_cast<const uint16_t *>(a.cache) + latent_row(a, b, j) * (a.dc + a.dr) + 8 * lane;
+    if (8 * lane < a.dc)
+      *reinterpret_cast<u32x4 *>(ws.c + (int64_t)(off + j) * a.dc + 8 * lane) = *reinterpret_cast<const u32x4 *>(row);
+    if (8 * lane < a.dr)
+      *reinterpret_cast<u32x4 *>(ws.kr + (int64_t)(off + j) * a.dr + 8 * lane) =
+          *reinterpret_cast<const u32x4 *>(row + a.dc);
   }
 }
 
@@ -87,7 +90,7 @@ struct Prompt {
 template <typename E, int DN, int DR, int DV>
 __global__ __launch_bounds__(512, 1) void latent_prompt_kernel(LatentArgs a, PromptWs ws, float c2, uint32_t flip) {
   using C = Prompt<DN, DR, DV>;
-  constexpr int kNT = C::kNT, kTB = C::kTB, kNB = C::kNB, DX = DN + DV;
+  constexpr int kNT = C::kNT, kTB = C::kTB, kNB = C::kNB, DX = DN + DV, kAhead = 4;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kBufs * C::kTileB];
   // an XCD (ids go round the 8 of them) takes whole heads, so that workgroups that share keys share an L2; late
   // tiles, which see the most, go first
@@ -105,8 +108,7 @@ __global__ __launch_bounds__(512, 1) void latent_prompt_kernel(LatentArgs a, Pro
   const int t = s.t0 + min(qi, s.nq - 1);
   const int last = min(s.nq, i0 + kRows) - 1;                          // the workgroup's last query
   const int n = (max(0, min(s.len, s.before + last + 1)) + kNT - 1) / kNT;  // tiles it sees
-  // what the wave sees: all rows up to w_all, none from w_end on
-  const int w_all = s.before + i0 + wave * 32 + 1;
+  // nothing from position w_end on is seen by the wave
   const int w_end = min(s.len, s.before + min(s.nq, i0 + wave * 32 + 32));
   const bool any = i0 + wave * 32 < s.nq;
 
@@ -127,21 +129,33 @@ __global__ __launch_bounds__(512, 1) void latent_prompt_kernel(LatentArgs a, Pro
   const int ld_unit = (lane & 7) ^ swz((8 * rb + ld_row) & 15);
   const uint8_t *xh = reinterpret_cast<const uint8_t *>(ws.x) + ((int64_t)h * ws.n_kv + off0) * (DX * 2);
   const uint8_t *kr = reinterpret_cast<const uint8_t *>(ws.kr) + (int64_t)off0 * (DR * 2);
-  auto load = [&](int i) {  // positions behind the last row repeat it
-    const int j0 = min(i * kNT + 8 * rb, (s.len - 1) & ~7);
+  // tile i: prepared, then loaded panel by panel; positions behind the last row repeat it, behind the last tile
+  // nothing is loaded (but counted)
+  const uint8_t *x_src = nullptr, *k_src = nullptr;
+  uint32_t to = 0;
+  int on = 0;
+  auto prepare = [&](int i) {
+    const int j0 = uniform(min(i * kNT + 8 * rb, max(s.len - 1, 0) & ~7));
     const int row = min(ld_row, s.len - 1 - j0);
-    const uint32_t to = uniform(lds0 + (i % C::kBufs) * C::kTileB + rb * 1024);
-    const uint8_t *x0 = uniform(xh + (int64_t)j0 * (DX * 2)), *k0 = uniform(kr + (int64_t)j0 * (DR * 2));
-    const uint32_t xo = row * (DX * 2) + ld_unit * 16, ko = row * (DR * 2) + (DR == 64 ? ld_unit : ld_unit & 3) * 16;
-    // panels: keys, rotary keys, values; with tiles of 32 tokens two waves share a block of 8
-    constexpr int kStep = 64 / kNT;
-#pragma unroll
-    for (int g = 0; g < C::kPK + C::kPV; g += kStep) {
-      const int gg = kStep == 1 ? g : g + uniform(wave >> 2);
-      if (gg == C::kPN)
-        lds_load16_s(k0, ko, to + gg * C::kPanelB);
+    x_src = uniform(xh + (int64_t)j0 * (DX * 2)) + (row * (DX * 2) + ld_unit * 16);
+    k_src = uniform(kr + (int64_t)j0 * (DR * 2)) + (row * (DR * 2) + (DR == 64 ? ld_unit : ld_unit & 3) * 16);
+    to = uniform(lds0 + (i % C::kBufs) * C::kTileB + rb * 1024);
+    on = uniform(i < n ? -1 : 0);
+  };
+  // panels: keys, rotary keys, values; with tiles of 32 tokens two waves share a block of 8 and take every other one
+  constexpr int kStep = 64 / kNT;
+  const int odd_wave = kStep == 1 ? 0 : uniform(wave >> 2);
+  auto load = [&](auto i) {
+    constexpr int g = i * kStep;
+    if constexpr (kStep == 1) {
+      if constexpr (g == C::kPN)
+        lds_load16<0>(k_src, to + g * C::kPanelB, on);
       else
-        lds_load16_s(uniform(x0 + (gg < C::kPN ? gg : gg - 1) * 128), xo, to + gg * C::kPanelB);
+        lds_load16<(g < C::kPN ? g : g - 1) * 128>(x_src, to + g * C::kPanelB, on);
+    } else {
+      const int gg = g + odd_wave;
+      const uint8_t *p = gg == C::kPN ? k_src : x_src + (gg < C::kPN ? gg : gg - 1) * 128;
+      lds_load16<0>(p, uniform(to + gg * C::kPanelB), on);
     }
   };
   int k_off[4], v_off[2][2];
@@ -159,29 +173,52 @@ __global__ __launch_bounds__(512, 1) void latent_prompt_kernel(LatentArgs a, Pro
 #pragma unroll
   for (int i = 0; i < kNB; ++i) acc[i] = f32x16{};
   float m = -__builtin_inff(), l = 0.0f;
+  if (n > 0)
 #pragma unroll
-  for (int i = 0; i < C::kBufs - 1; ++i)
-    if (i < n) load(i);
+    for (int i = 0; i < C::kBufs - 1; ++i) {
+      prepare(i);
+      static_for<0, C::kLoads>(load);
+    }
   for (int it = 0; it < n; ++it) {
-    if (it + 1 < n)
-      WAIT_VM(C::kLoads);
-    else
-      WAIT_VM(0);
+    WAIT_VM((C::kBufs - 2) * C::kLoads);
     asm volatile("s_barrier" ::: "memory");
-    if (it + 2 < n) load(it + 2);
+    prepare(it + C::kBufs - 1);
     const int j0 = it * kNT;
     const bool masked = j0 + kNT > s.before + i0 + 1;  // the same in every wave: some row of the workgroup does not see all
-    if (!masked && !any) continue;
+    if (!masked && !any) {
+      static_for<0, C::kLoads>(load);
+      continue;
+    }
     uint8_t *kv = lds + (it % C::kBufs) * C::kTileB, *vv = kv + C::kPK * C::kPanelB;
+    // Operands are read kAhead products before they are used, the next tile's loads go in between, and the order is
+    // held (see latent_attend.hip).
+    constexpr int kZ = C::kKS * kTB, kV = 2 * kTB * kNB;  // products
+    auto k_read = [&](int i) {
+      const int k = i / kTB, tb = i % kTB;
+      return *reinterpret_cast<const u16x8 *>(kv + k_off[k & 3] + (k >> 2) * C::kPanelB + tb * 32 * 128);
+    };
+    auto v_read = [&](int i) {
+      const int ks = i / kNB, nb = i % kNB;
+      const uint8_t *src = vv + (nb >> 1) * C::kPanelB + ks * 16 * 128;
+      const u16x4 lo = lds_read_tr(src + v_off[0][nb & 1]), hi = lds_read_tr(src + v_off[1][nb & 1]);
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
     f32x16 z[kTB];
 #pragma unroll
     for (int tb = 0; tb < kTB; ++tb) z[tb] = f32x16{};
+    u16x8 ring[kAhead];
 #pragma unroll
-    for (int k = 0; k < C::kKS; ++k)
-#pragma unroll
-      for (int tb = 0; tb < kTB; ++tb)
-        z[tb] = E::mfma(*reinterpret_cast<const u16x8 *>(kv + k_off[k & 3] + (k >> 2) * C::kPanelB + tb * 32 * 128), q[k],
-                        z[tb]);
+    for (int i = 0; i < kAhead; ++i) ring[i] = k_read(i);
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<0, kZ>([&](auto i) {
+      z[i % kTB] = E::mfma(ring[i % kAhead], q[i / kTB], z[i % kTB]);
+      if (i + kAhead < kZ)
+        ring[i % kAhead] = k_read(i + kAhead);
+      else if (i + kAhead - kZ < kV)
+        ring[i % kAhead] = v_read(i + kAhead - kZ);
+      if constexpr (i % 2 == 1 && i / 2 < C::kLoads) load(std::integral_constant<int, i / 2>{});
+      __builtin_amdgcn_sched_barrier(0);
+    });
     if (masked) {
       // tokens the lane's row sees, as bits
       const uint64_t vis64 = [&] {
@@ -222,6 +259,8 @@ __global__ __launch_bounds__(512, 1) void latent_prompt_kernel(LatentArgs a, Pro
             z[tb][i] = (bad >> (32 * tb + 8 * (i >> 2) + 4 * hl + (i & 3))) & 1 ? -__builtin_inff() : z[tb][i];
         if (bad & (kNT == 64 ? ~0ull : 0xffffffffull) & (vis64 << (4 * hl))) l = __builtin_nanf("");
         __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kAhead && i < kV; ++i) ring[(kZ + i) % kAhead] = v_read(i);  // once more
       }
     }
     if (j0 >= w_end) continue;  // nothing of this tile is seen by the wave
@@ -241,41 +280,39 @@ __global__ __launch_bounds__(512, 1) void latent_prompt_kernel(LatentArgs a, Pro
       for (int i = 0; i < kNB; ++i) acc[i] *= f;
     }
     const float base = m == -__builtin_inff() ? 0.0f : -m;
-    u16x8 p[2 * kTB];
+    // the weights of 16 tokens at a time, each group's between the products of the group before
+    auto weight = [&](int i) {
+      const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i / 16][i % 16], c2, base));
+      l += e;
+      return e;
+    };
+    f32x8 e;
 #pragma unroll
-    for (int tb = 0; tb < kTB; ++tb)
+    for (int i = 0; i < 8; ++i) e[i] = weight(i);
+    u16x8 p = E::from_f32x8(e);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        f32x8 e;
+    for (int i = 0; i < kV; ++i) {
+      const int ks = i / kNB, nb = i % kNB;
+      if (ks && nb == 0) p = E::from_f32x8(e);
+      acc[nb] = E::mfma(ring[(kZ + i) % kAhead], p, acc[nb]);
+      if (i + kAhead < kV) ring[(kZ + i) % kAhead] = v_read(i + kAhead);
+      if (ks + 1 < 2 * kTB)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[tb][8 * half + i], c2, base));
-          l += e[i];
-        }
-        p[2 * tb + half] = E::from_f32x8(e);
-      }
-#pragma unroll
-    for (int ks = 0; ks < 2 * kTB; ++ks)
-#pragma unroll
-      for (int nb = 0; nb < kNB; ++nb) {
-        const uint8_t *src = vv + (nb >> 1) * C::kPanelB + ks * 16 * 128;
-        const u16x4 lo = lds_read_tr(src + v_off[0][nb & 1]), hi = lds_read_tr(src + v_off[1][nb & 1]);
-        acc[nb] = E::mfma(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), p[ks], acc[nb]);
-      }
+        for (int j = nb * 8 / kNB; j < (nb + 1) * 8 / kNB; ++j) e[j] = weight(8 * (ks + 1) + j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
-  (void)w_all;
   l += __shfl_xor(l, 32, 64);
-  if (!live) return;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t *o = static_cast<uint16_t *>(a.out) + ((int64_t)t * a.H + h) * DV + 4 * hl;
+  uint16_t *o = static_cast<uint16_t *>(a.out) + ((int64_t)t * a.H + h) * DV + 8 * hl;
 #pragma unroll
   for (int i = 0; i < kNB; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      u16x4 v;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = E::from_f32(acc[i][4 * j + e] * inv);
-      *reinterpret_cast<u16x4 *>(o + 32 * i + 8 * j) = v;
+    for (int j = 0; j < 4; j += 2) {
+      const f32x16 r = acc[i] * inv;
+      const u32x4 v = rows8<E>(f32x4{r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]},
+                               f32x4{r[4 * j + 4], r[4 * j + 5], r[4 * j + 6], r[4 * j + 7]});
+      if (live) *reinterpret_cast<u32x4 *>(o + 32 * i + 8 * j) = v;
     }
 }
 
@@ -284,25 +321,25 @@ moe_status launch(moe_ctx *ctx, const LatentArgs &a, int64_t n_kv) {
   const int64_t tiles = a.T / kRows + a.B;  // at most: every sequence adds one tile that is not full
   MoeLayout lay;
   const size_t o_off = lay.take(4 * (size_t)(a.B + 1)), o_nt = lay.take(4), o_tile = lay.take(sizeof(PromptTile) * tiles),
-               o_rows = lay.take(8 * (size_t)n_kv), o_kr = lay.take(2 * (size_t)n_kv * DR),
+               o_c = lay.take(2 * (size_t)n_kv * a.dc), o_kr = lay.take(2 * (size_t)n_kv * DR),
                o_x = lay.take(2 * (size_t)n_kv * a.H * (DN + DV));
   void *scr = nullptr;
   moe_status st = moe_scratch(ctx, lay.size, &scr);
   if (st) return st;
   char *p = static_cast<char *>(scr);
   const PromptWs ws{reinterpret_cast<int32_t *>(p + o_off),  reinterpret_cast<int32_t *>(p + o_nt),
-                    reinterpret_cast<PromptTile *>(p + o_tile), reinterpret_cast<int64_t *>(p + o_rows),
+                    reinterpret_cast<PromptTile *>(p + o_tile), reinterpret_cast<uint16_t *>(p + o_c),
                     reinterpret_cast<uint16_t *>(p + o_kr),  reinterpret_cast<uint16_t *>(p + o_x),
                     n_kv};
   hipLaunchKernelGGL(prompt_plan_kernel, dim3(1), dim3(1024), 0, ctx->stream, a, ws);
   MOE_CHECK_LAUNCH("prompt_plan_kernel");
   if (n_kv > 0) {
-    hipLaunchKernelGGL(prompt_rows_kernel, dim3(16, a.B), dim3(256), 0, ctx->stream, a, ws);
+    const unsigned row_blocks = (unsigned)std::max<int64_t>(1, std::min<int64_t>(n_kv / 4, 2048) / a.B);
+    hipLaunchKernelGGL(prompt_rows_kernel, dim3(row_blocks, a.B), dim3(256), 0, ctx->stream, a, ws);
     MOE_CHECK_LAUNCH("prompt_rows_kernel");
-    const HeadGemm expand{static_cast<const uint16_t *>(a.cache), static_cast<const uint16_t *>(a.w_kv), ws.x, ws.rows,
-                          nullptr, ws.off + a.B, (int)n_kv, DN + DV, a.dc, a.dc + DR, 0, (int64_t)(DN + DV) * a.dc,
-                          DN + DV, n_kv * (DN + DV), 16};
-    if ((st = launch_head_gemm(ctx, E::kDtype, expand, a.H, LatentPlan{}))) return st;
+    const ExpandGemm expand{ws.c, static_cast<const uint16_t *>(a.w_kv), ws.x, ws.off + a.B, (int)n_kv, a.H, DN + DV,
+                            a.dc};
+    if ((st = launch_expand_gemm(ctx, E::kDtype, expand))) return st;
   }
   const float c2 = latent_c2(a.scale);
   hipLaunchKernelGGL((latent_prompt_kernel<E, DN, DR, DV>), dim3((unsigned)(tiles * ((a.H + 7) / 8) * 8)), dim3(512), 0,

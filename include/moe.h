@@ -511,7 +511,7 @@ typedef struct {
 
 /* What both forms take. q_nope[t * nope_t + h * nope_h + i] (strides in
  * elements, multiples of 8), q_rope likewise; all DEVICE pointers.
- * T <= 2^20 tokens, B <= 1024 sequences. out [T][n_heads][d_v] may be no input.
+ * T <= 2^20 tokens, B <= 1024 sequences, n_pages * page_size <= 2^31. out [T][n_heads][d_v] may be no input.
  * Checked on the device, reported by moe_ctx_check as MOE_EINVAL, without a
  * read or write outside the arrays: q_start not ascending within 0..T, kv_len
  * negative or above max_pages * page_size, page ids outside [0, n_pages) (the

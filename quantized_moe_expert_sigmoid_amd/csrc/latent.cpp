@@ -72,6 +72,8 @@ static moe_status call_args(const char *fn, moe_ctx *ctx, const moe_latent_cfg *
           "%s: query strides must be multiples of 8", fn);
   REQUIRE(call->max_pages >= 0 && call->n_pages >= 0 && call->n_pages <= (int64_t)1 << 31,
           "%s: max_pages %d, n_pages %lld", fn, call->max_pages, (long long)call->n_pages);
+  REQUIRE(call->n_pages * c->page_size <= (int64_t)1 << 31, "%s: %lld pages of %d rows: above 2^31 rows", fn,
+          (long long)call->n_pages, c->page_size);
   REQUIRE((int64_t)call->max_pages * c->page_size <= (int64_t)1 << 30, "%s: max_pages %d of %d rows: above 2^30 rows",
           fn, call->max_pages, c->page_size);
   if (call->T == 0 || call->B == 0) return MOE_OK;

@@ -44,8 +44,9 @@ moe_status launch_latent_prompt(moe_ctx *ctx, int dtype, const LatentArgs &a, in
 
 // How the absorbed form's work is shared out (see latent_attend.hip), written
 // by one workgroup of the kernel that absorbs the queries.
-struct WgDesc {
-  int b, mt, at, n;  // first unit: sequence, row tile, place in the row tile's units; number of units
+struct alignas(32) WgDesc {
+  int b, mt, at, n;       // first unit: sequence, row tile, place in the row tile's units; number of units
+  int t0, nq, len, over;  // the sequence's bounds; units a row tile has ahead of its cache tiles
 };
 struct TileDesc {
   int b, mt, w0, w1;  // a row tile whose cache tiles several workgroups share, and those
@@ -53,7 +54,6 @@ struct TileDesc {
 };
 struct PlanHead {
   int64_t per;   // units of a workgroup
-  int over;      // units a row tile has ahead of its cache tiles
   int n_shared;  // TileDescs
 };
 struct LatentPlan {
@@ -156,15 +156,32 @@ struct Fp16 {
 // matrix instructions inside assembly, so the waits it would add stand here: two
 // wait states from a vector write to a product that reads it, and settle()
 // before the accumulators are read back.
+template <typename E, bool PINNED>
+struct AccTile {  // few of them: ordinary variables
+  f32x16 c;
+  __device__ __forceinline__ void mfma(u16x8 a, u16x8 b, bool) { c = E::mfma(a, b, c); }
+  __device__ __forceinline__ void scale(float f) { c *= f; }
+  __device__ __forceinline__ f32x4 get4(int j) const { return f32x4{c[4 * j], c[4 * j + 1], c[4 * j + 2], c[4 * j + 3]}; }
+};
+template <typename E, int N>
+__device__ __forceinline__ void settle(AccTile<E, false> (&)[N]) {}
+template <typename E, int N>
+__device__ __forceinline__ void clear(AccTile<E, false> (&t)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) t[i].c = f32x16{};
+}
+
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass does not know the register class
 template <typename E>
-struct AccTile {
+struct AccTile<E, true> {
   f32x16 c;
-  __device__ __forceinline__ void mfma(u16x8 a, u16x8 b) {
+  // c += a b; fresh: an operand may have been written by the vector instruction just before
+  __device__ __forceinline__ void mfma(u16x8 a, u16x8 b, bool fresh) {
+    if (fresh) asm("s_nop 1" : "+v"(a), "+v"(b));
     if constexpr (E::kDtype == MOE_BF16)
-      asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+      asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
     else
-      asm("s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+      asm("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
   }
   __device__ __forceinline__ void scale(float f) {
 #pragma unroll
@@ -184,7 +201,7 @@ struct AccTile {
   __device__ __forceinline__ f32x4 get4(int j) const { return f32x4{get(4 * j), get(4 * j + 1), get(4 * j + 2), get(4 * j + 3)}; }
 };
 template <typename E, int N>
-__device__ __forceinline__ void settle(AccTile<E> (&t)[N]) {
+__device__ __forceinline__ void settle(AccTile<E, true> (&t)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+a"(t[i].c));
   asm volatile("s_nop 15\n\ts_nop 15");  // a 32x32x16 product's result is readable after at most 18 states
@@ -192,7 +209,7 @@ __device__ __forceinline__ void settle(AccTile<E> (&t)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+a"(t[i].c));
 }
 template <typename E, int N>
-__device__ __forceinline__ void clear(AccTile<E> (&t)[N]) {
+__device__ __forceinline__ void clear(AccTile<E, true> (&t)[N]) {
   const u16x8 z = {};
 #pragma unroll
   for (int i = 0; i < N; ++i)  // volatile: a product each, not one value copied about
@@ -201,16 +218,16 @@ __device__ __forceinline__ void clear(AccTile<E> (&t)[N]) {
 }
 #else
 template <typename E>
-struct AccTile {
-  __device__ void mfma(u16x8 a, u16x8 b);
+struct AccTile<E, true> {
+  __device__ void mfma(u16x8 a, u16x8 b, bool fresh);
   __device__ void scale(float f);
   __device__ float get(int e) const;
   __device__ f32x4 get4(int j) const;
 };
 template <typename E, int N>
-__device__ void settle(AccTile<E> (&t)[N]);
+__device__ void settle(AccTile<E, true> (&t)[N]);
 template <typename E, int N>
-__device__ void clear(AccTile<E> (&t)[N]);
+__device__ void clear(AccTile<E, true> (&t)[N]);
 #endif
 
 // Results of a 32 x 32 product, four consecutive rows a lane, as elements: the
@@ -283,7 +300,7 @@ __device__ __forceinline__ LatentSeq latent_seq(const LatentArgs &a, int b) {
   s.before = s.len - s.nq;
   return s;
 }
-// Cache row of position j (< len) of sequence b; a page id out of range is
+// Cache row of position j (< len, rows fit 31 bits) of sequence b; a page id out of range is
 // reported and row 0 taken.
 __device__ __forceinline__ int64_t latent_row(const LatentArgs &a, int b, int j) {
   const int p = a.page_table[(int64_t)b * a.max_pages + (j >> a.page_shift)];

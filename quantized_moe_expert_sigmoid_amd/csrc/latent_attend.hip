@@ -21,13 +21,19 @@ namespace {
 
 constexpr int kNT = 32;  // tokens of a cache tile
 
-// A unit of work is one cache tile for one row tile. Units are numbered sequence
-// by sequence, row tile by row tile, cache tile by cache tile, each row tile
-// with up to kOver units ahead of its cache tiles for what starting and ending
-// it costs; workgroup w takes units [w per, (w + 1) per), so that all have about
-// the same work whatever the lengths are. A row tile whose cache tiles several
-// workgroups share is joined from their partial results by the merge kernel.
-constexpr int kOver = 6;
+// A unit of work is one cache tile for one row tile. Where there are fewer row
+// tiles than workgroups, each row tile's cache tiles are cut into equal pieces,
+// as many as the workgroups allow, and a workgroup takes one piece: it then
+// starts and ends one run only, which costs about as much as kOver cache tiles
+// (queries and first tiles to wait for, a partial result of 2 KB a row to write).
+// Where that leaves some with kOver tiles more than even work, and where there
+// are more row tiles, units are numbered sequence by sequence, row tile by row
+// tile, cache tile by cache tile, each row tile with kOver units ahead of its
+// cache tiles, and workgroup w takes units [w per, (w + 1) per). Either way the
+// lengths are read on the device and all workgroups have about the same work. A
+// row tile whose cache tiles several workgroups share is joined from their
+// partial results by the merge kernel.
+constexpr int kOver = 12;
 
 struct AttendWs {
   const PlanHead *head;
@@ -62,16 +68,19 @@ struct Attend {
   static constexpr int kQL = kNB >= 16 ? kKS / 3 : 0;
   static constexpr bool in_lds(int k) { return kQL && k % 3 == 2; }
   static_assert(!kQL || kQL == kKS / 3, "");
-  static constexpr int kBufs = kQL ? 3 : 4;      // tile buffers: one being read, the others in flight
+  static constexpr int kBufs = kQL || DC < 512 ? 3 : 4;  // tile buffers: one being read, the others in flight
   static constexpr int kQB = kWaves * kQL * 1024;
   static constexpr int kLds = kBufs * kTileB + kQB;
-  static_assert(kWaves == 4 && kLds <= 160 << 10, "4 waves load a tile's 32 tokens, 8 each");
+  // small rows of few registers: two workgroups a CU, so that one computes while the other starts or ends a run
+  static constexpr int kPerCu = DC < 512 && kNB <= 4 ? 2 : 1;
+  static_assert(kWaves == 4 && kPerCu * kLds <= 160 << 10, "4 waves load a tile's 32 tokens, 8 each");
 };
 
 template <typename E, int DC, int DR, int WM, int WN>
-__global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, AttendWs ws, float c2, uint32_t flip) {
+__global__ __launch_bounds__(256, (Attend<DC, DR, WM, WN>::kPerCu)) void latent_attend_kernel(
+    LatentArgs a, AttendWs ws, float c2, uint32_t flip) {
   using C = Attend<DC, DR, WM, WN>;
-  constexpr int kNB = C::kNB, kBufs = C::kBufs, kPanels = C::kPanels, kAhead = 6;
+  constexpr int kNB = C::kNB, kBufs = C::kBufs, kPanels = C::kPanels, kAhead = C::kPerCu == 2 ? 4 : 6, kChains = 2;
   constexpr int kLoadStep = (C::kKS - 4) / kPanels;  // a panel's load every so many products
   __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLds];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -79,7 +88,8 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
   // neighbours in the unit order share cache rows: keep them on one XCD (ids go round the 8 XCDs)
   const int w = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
   const WgDesc d = ws.wg[w];
-  const int over = uniform(ws.head->over);
+  const int over = uniform(d.over);
+  LatentSeq s{uniform(d.t0), uniform(d.nq), uniform(d.len), uniform(d.len) - uniform(d.nq)};
   int b = uniform(d.b), mt = uniform(d.mt), at = uniform(d.at), left = uniform(d.n);
   bool first = true;
   const uint8_t *cache = static_cast<const uint8_t *>(a.cache);
@@ -102,8 +112,6 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
                      (((4 * (p ^ (kNB == 1 ? wn & 1 : 0)) + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ swz(vt + 8 * h8)) << 4) + (lane & 1) * 8;
 
   while (left > 0) {
-    const LatentSeq r = latent_seq(a, b);
-    const LatentSeq s{uniform(r.t0), uniform(r.nq), uniform(r.len), uniform(r.before)};
     const int nt = row_tiles(a, s, C::kMT), kts = kv_tiles(s);
     const int units = min(left, kts + over - at);                        // of this row tile
     const int kt = max(at - over, 0), n = max(at + units - over, 0) - kt;  // first cache tile, cache tiles
@@ -127,40 +135,35 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
 
       // The wave's 8 tokens of tile i of this run, into its buffer: prepared, then loaded panel by panel. Positions
       // behind the sequence's last row repeat that row; behind the run's last tile nothing is loaded (but counted).
-      // Pages of 8 rows and more hold all 8 tokens: lane i then keeps the page of tile i of 64, so that a tile's page
-      // costs no memory access of its own.
-      auto first_of = [&](int i) { return min((kt + i) * kNT + 8 * wave, (s.len - 1) & ~7); };
+      // The pages come from a lane each: of 64 tiles where a page holds a tile's 8 tokens, of 8 tiles' 8 tokens
+      // where it does not, so that a tile's pages cost no memory access of its own.
+      const bool small = a.page_shift < 3;
       int pages = 0;
       auto read_pages = [&](int i) {
-        pages = a.page_table[(int64_t)b * a.max_pages + (first_of(i + lane) >> a.page_shift)];
+        const int j = small ? (kt + i + (lane >> 3)) * kNT + 8 * wave + (lane & 7) : (kt + i + lane) * kNT + 8 * wave;
+        pages = a.page_table[(int64_t)b * a.max_pages + (min(j, s.len - 1) >> a.page_shift)];
         if (pages < 0 || pages >= a.n_pages) {
           atomicOr(a.err, (uint32_t)ERRF_LATENT);
           pages = 0;
         }
       };
       const uint8_t *src = nullptr;
-      uint32_t to = 0;
-      int on = 0, j0_next = 0, r_next = 0;
-      int64_t row_next = 0;
+      uint32_t to = 0, place = lds0 + wave * 1024;
+      int on = 0, j_next = 0, page_next = 0;
       auto prepare = [&](int i, auto part) {  // in four parts, for between the products
         if constexpr (part == 0) {
-          j0_next = uniform(first_of(i));
-          r_next = min(ld_row, s.len - 1 - j0_next);
-          on = uniform(i < n ? -1 : 0);
+          if ((i & (small ? 7 : 63)) == 0) read_pages(i);
+          // a tile that lies behind the last row altogether repeats that row
+          const int j0 = min((kt + i) * kNT + 8 * wave, s.len - 1), r = min(ld_row, s.len - 1 - j0);
+          j_next = j0 + r;
+          page_next = __shfl(pages, small ? (i & 7) * 8 + r : i & 63, 64);
         } else if constexpr (part == 1) {
-          if (a.page_shift >= 3) {
-            if ((i & 63) == 0) read_pages(i);
-            const int page = __builtin_amdgcn_readlane(pages, i & 63);
-            row_next = ((int64_t)page << a.page_shift) + (j0_next & ((1 << a.page_shift) - 1));
-          } else {
-            row_next = latent_row(a, b, j0_next + r_next);
-            r_next = 0;
-          }
+          to = place;
+          place = place - lds0 >= (uint32_t)((kBufs - 1) * C::kTileB) ? place - (kBufs - 1) * C::kTileB : place + C::kTileB;
+          on = (i - n) >> 31;
         } else if constexpr (part == 2) {
-          to = uniform(lds0 + (i % kBufs) * C::kTileB + wave * 1024);
-          src = cache + row_next * (C::kDK * 2);
-        } else {
-          src += r_next * (C::kDK * 2) + ld_unit * 16;
+          const uint32_t row = ((uint32_t)page_next << a.page_shift) + (j_next & ((1 << a.page_shift) - 1));
+          src = cache + (uint64_t)row * (C::kDK * 2) + ld_unit * 16;
         }
       };
       auto load = [&](auto g) {
@@ -174,7 +177,7 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
       if (s.len > 0)
 #pragma unroll
         for (int i = 0; i < kBufs - 1; ++i) {
-          static_for<0, 4>([&](auto part) { prepare(i, part); });
+          static_for<0, 3>([&](auto part) { prepare(i, part); });
           static_for<0, kPanels>(load);
         }
       u16x8 q[C::kKS - C::kQL];
@@ -193,7 +196,7 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
         }
       }
 
-      AccTile<E> acc[kNB];
+      AccTile<E, (kNB > 4)> acc[kNB];
       clear(acc);
       float m = -__builtin_inff(), l = 0.0f;
       if (s.len > 0)
@@ -209,7 +212,9 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
           u16x8 ring[kAhead];
           // Operands are read kAhead products before they are used, and the order is held: left to itself the
           // compiler reads each one just before its product and waits for it.
-          f32x16 z = {}, z1 = {};
+          f32x16 zs[kChains];
+#pragma unroll
+          for (int i = 0; i < kChains; ++i) zs[i] = f32x16{};
           {
             auto k_read = [&](int k) {
               return *reinterpret_cast<const u16x8 *>(kv + k_off[k & 3] + (k >> 2) * C::kPanelB);
@@ -227,23 +232,22 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
             // operands.
             static_for<0, C::kKS>([&](auto k) {
               const u16x8 qk = C::in_lds(k) ? qf[k / 3 & 1] : q[C::kQL ? k - k / 3 : k];
-              if (k & 1)
-                z1 = E::mfma(ring[k % kAhead], qk, z1);
-              else
-                z = E::mfma(ring[k % kAhead], qk, z);
+              zs[k % kChains] = E::mfma(ring[k % kAhead], qk, zs[k % kChains]);
               if (k + kAhead < C::kKS)
                 ring[k % kAhead] = k_read(k + kAhead);
               else if (k + kAhead - C::kKS < 2 * kNB)
                 ring[k % kAhead] = v_read(k + kAhead - C::kKS);
               if (C::in_lds(k) && k / 3 + 2 < C::kQL) qf[k / 3 & 1] = q_lds[(k / 3 + 2) * 64];
-              if constexpr (k < 4)
+              if constexpr (k < 3)
                 prepare(it + kBufs - 1, k);
               else if constexpr ((k - 4) % kLoadStep == 0 && (k - 4) / kLoadStep < kPanels)
                 load(std::integral_constant<int, (k - 4) / kLoadStep>{});
               __builtin_amdgcn_sched_barrier(0);
             });
           }
-          z += z1;
+          f32x16 z = zs[0];
+#pragma unroll
+          for (int i = 1; i < kChains; ++i) z += zs[i];
           const int j0 = (kt + it) * kNT;
           if (j0 + kNT > s.before) {  // the tile holds tokens that not every row sees
             const uint32_t vis = seen(j0) >> (4 * hl);
@@ -311,7 +315,7 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
 #pragma unroll
           for (int i = 0; i < 2 * kNB; ++i) {
             if (i == kNB) p = E::from_f32x8(e);
-            acc[i % kNB].mfma(ring[(C::kKS + i) % kAhead], p);
+            acc[i % kNB].mfma(ring[(C::kKS + i) % kAhead], p, i % kNB == 0);
             if (i + kAhead < 2 * kNB) ring[(C::kKS + i) % kAhead] = v_read(i + kAhead);
             if (i < kNB)
 #pragma unroll
@@ -349,6 +353,10 @@ __global__ __launch_bounds__(256, 1) void latent_attend_kernel(LatentArgs a, Att
     if (nt == 0 || ++mt == nt) {
       mt = 0;
       ++b;
+      if (left > 0) {
+        const LatentSeq r = latent_seq(a, b);
+        s = LatentSeq{uniform(r.t0), uniform(r.nq), uniform(r.len), uniform(r.before)};
+      }
     }
   }
 }
@@ -473,7 +481,7 @@ __global__ __launch_bounds__(256) void latent_merge_kernel(LatentArgs a, AttendW
 template <typename E, int DC, int DR, int WM, int WN>
 moe_status launch(moe_ctx *ctx, const LatentArgs &a) {
   using C = Attend<DC, DR, WM, WN>;
-  const int n_wg = ctx->n_cu / 8 * 8;  // a workgroup a CU: its buffers and accumulators fill one
+  const int n_wg = ctx->n_cu / 8 * 8 * C::kPerCu;  // whole multiples of the 8 XCDs
   MoeLayout lay;
   const size_t o_head = lay.take(sizeof(PlanHead)), o_wg = lay.take(sizeof(WgDesc) * n_wg),
                o_shared = lay.take(sizeof(TileDesc) * n_wg),

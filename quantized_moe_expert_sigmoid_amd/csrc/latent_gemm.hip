@@ -38,54 +38,97 @@ __device__ int last_at_or_below(const int64_t *cum, int n, int64_t v) {  // cum 
   return lo;
 }
 
+// Two ways to share the units out (see latent_attend.hip): pieces of row tiles, a
+// piece a workgroup, where there are fewer row tiles than workgroups and the
+// largest piece is not much above even work; even runs otherwise.
 __device__ void make_plan(const LatentPlan &p, uint8_t *lds) {
   constexpr int kPer = 4;  // sequences a thread
-  int64_t *units = reinterpret_cast<int64_t *>(lds), *tmp = units + 1024;
+  int64_t *start = reinterpret_cast<int64_t *>(lds), *tmp = start + 1024;  // of a sequence's units, or pieces
+  int *t0s = reinterpret_cast<int *>(tmp + 8), *nqs = t0s + 1024, *lens = nqs + 1024;
   const int tid = threadIdx.x;
-  int64_t u = 0, uu[kPer], rt = 0, rr[kPer];
+  auto tiles_of = [&](int len) { return max(1, (len + p.tokens - 1) / p.tokens); };
+  int64_t u = 0, rt = 0;
+  int rr[kPer], kk[kPer];  // row tiles, cache tiles
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int b = tid * kPer + i;
-    uu[i] = rr[i] = 0;
+    rr[i] = 0;
+    kk[i] = 1;
     if (b < p.a.B) {
       const LatentSeq s = latent_seq(p.a, b);
-      rr[i] = ((int64_t)s.nq * p.a.H + p.rows - 1) / p.rows;
-      uu[i] = rr[i] * max(1, (s.len + p.tokens - 1) / p.tokens);
+      t0s[b] = s.t0;
+      nqs[b] = s.nq;
+      lens[b] = s.len;
+      rr[i] = (s.nq * p.a.H + p.rows - 1) / p.rows;
+      kk[i] = tiles_of(s.len);
     }
-    u += uu[i];
+    u += (int64_t)rr[i] * kk[i];
     rt += rr[i];
   }
-  int64_t total, n_rows, u0 = scan_excl<int64_t>(u, tmp, total);
-  const int64_t r0 = scan_excl<int64_t>(rt, tmp, n_rows);
-  // where a workgroup has few cache tiles it is better off with fewer of them than with even work
-  const int over = total >= 8 * (int64_t)p.n_wg ? p.over : 0;
-  u0 += over * r0;
-  total += over * n_rows;
+  int64_t total, n_rows;
+  scan_excl<int64_t>(u, tmp, total);
+  scan_excl<int64_t>(rt, tmp, n_rows);
+  const int64_t even = (total + p.n_wg - 1) / p.n_wg;
+
+  // the smallest pieces that are no more than the workgroups
+  int piece = 0;
+  if (n_rows > 0 && n_rows < p.n_wg) {
+    int64_t lo = even, hi = min(even + p.over, (total + p.n_wg - n_rows - 1) / (p.n_wg - n_rows));
+    while (lo <= hi) {
+      const int64_t mid = (lo + hi) >> 1;
+      int64_t c = 0, n;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) c += (int64_t)rr[i] * ((kk[i] + mid - 1) / mid);
+      scan_excl<int64_t>(c, tmp, n);
+      if (n <= p.n_wg) {
+        piece = (int)mid;
+        hi = mid - 1;
+      } else {
+        lo = mid + 1;
+      }
+    }
+  }
+  // even runs: where a workgroup has few cache tiles it is better off with fewer of them than with even work
+  const int over = !piece && total >= 4 * (int64_t)p.n_wg ? p.over : 0;
+  int64_t mine = 0, all;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) mine += (int64_t)rr[i] * (piece ? (kk[i] + piece - 1) / piece : kk[i] + over);
+  int64_t at0 = scan_excl<int64_t>(mine, tmp, all);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    units[tid * kPer + i] = u0;
-    u0 += uu[i] + over * rr[i];
+    start[tid * kPer + i] = at0;
+    at0 += (int64_t)rr[i] * (piece ? (kk[i] + piece - 1) / piece : kk[i] + over);
   }
   __syncthreads();
-  const int64_t per = max((total + p.n_wg - 1) / p.n_wg, (int64_t)1);
+  const int64_t per = piece ? 1 : max((all + p.n_wg - 1) / p.n_wg, (int64_t)1);
   int shared0 = 0;
   for (int w0 = 0; w0 < p.n_wg; w0 += 256) {
     const int w = w0 + tid;
     const int64_t v = w * per;
-    WgDesc d{0, 0, 0, 0};
+    WgDesc d{};
     TileDesc t{};
-    if (w < p.n_wg && v < total) {
+    if (w < p.n_wg && v < all) {
       // the last sequence that starts at or before v is the one that has it: those without units share their
       // successor's start
-      const int b = last_at_or_below(units, 1024, v);
-      const LatentSeq s = latent_seq(p.a, b);
-      const int k = max(1, (s.len + p.tokens - 1) / p.tokens);
-      const int64_t r = v - units[b];
-      d = WgDesc{b, (int)(r / (k + over)), (int)(r % (k + over)), (int)min(per, total - v)};
-      // shared with the workgroups before, and the first boundary in this row tile
-      const int64_t u0 = v - d.at;
-      const int first = (int)((u0 + over) / per);
-      if (d.at > over && first == w - 1) t = TileDesc{b, d.mt, first, (int)((u0 + over + k - 1) / per), u0};
+      const int b = last_at_or_below(start, 1024, v);
+      const int k = tiles_of(lens[b]);
+      const uint32_t r = (uint32_t)min(v - start[b], (int64_t)0x7fffffff);
+      d = WgDesc{b, 0, 0, 0, t0s[b], nqs[b], lens[b], over};
+      if (piece) {
+        const int c = (k + piece - 1) / piece, i = r % (uint32_t)c;  // piece i of c of row tile mt
+        d.mt = r / (uint32_t)c;
+        d.at = (int)((int64_t)k * i / c);
+        d.n = (int)((int64_t)k * (i + 1) / c) - d.at;
+        if (i == 0 && c > 1) t = TileDesc{b, d.mt, w, w + c - 1, 0};
+      } else {
+        d.mt = r / (uint32_t)(k + over);
+        d.at = r % (uint32_t)(k + over);
+        d.n = (int)min(per, all - v);
+        // shared with the workgroups before, and the first boundary in this row tile
+        const int64_t u0 = v - d.at;
+        const int first = (int)((u0 + over) / per);
+        if (d.at > over && first == w - 1) t = TileDesc{b, d.mt, first, (int)((u0 + over + k - 1) / per), u0};
+      }
     }
     if (w < p.n_wg) p.wg[w] = d;
     int64_t n;
@@ -93,7 +136,7 @@ __device__ void make_plan(const LatentPlan &p, uint8_t *lds) {
     if (t.w1 > 0) p.shared[shared0 + at] = t;
     shared0 += (int)n;
   }
-  if (tid == 0) *p.head = PlanHead{per, over, shared0};
+  if (tid == 0) *p.head = PlanHead{per, shared0};
 }
 
 // --- many rows: tiles of 128 rows x 64 or 128 columns through LDS --------------
@@ -184,53 +227,53 @@ __global__ __launch_bounds__(256, 2) void head_gemm_tile_kernel(HeadGemm g, Late
 }
 
 // --- few rows: the weights' bytes are the bound ---------------------------------
-// A wave takes 32 rows x 32 columns and reads both operands from memory straight
-// in the products' layout (16 bytes a lane, a column's k in order), 128 k of
-// loads in flight before the products of the previous 128.
+// A workgroup takes 32 rows x 32 columns, each wave a quarter of k: both operands
+// come from memory straight in the products' layout (16 bytes a lane, a column's
+// k in order), all of a wave's loads in flight at once; the quarters are summed
+// through LDS.
+constexpr int kPlanLds = 8 * 1024 + 64 + 3 * 4096;
+
 template <typename E>
 __global__ __launch_bounds__(256) void head_gemm_stream_kernel(HeadGemm g, LatentPlan plan) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[8 * 1024 + 64];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kPlanLds > 16384 ? kPlanLds : 16384];
   if (plan.n_wg && blockIdx.x == gridDim.x - 1) {
     if (blockIdx.y == 0 && blockIdx.z == 0) make_plan(plan, lds);
     return;
   }
-  const int M = g.hi ? min(g.M, uniform(*g.hi)) : g.M, lo = g.lo ? uniform(*g.lo) : 0;
-  const int m0 = blockIdx.z * 32;
-  const int lane = threadIdx.x & 63, n0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * 32, h = blockIdx.y;
-  if (m0 >= M || m0 + 32 <= lo || n0 >= g.N) return;
-  const int l32 = lane & 31, hl = lane >> 5;
-  const int m = m0 + l32;
-  const int ma = min(m, M - 1);
-  const uint16_t *a = g.A + (int64_t)ma * g.a_m + h * g.a_h + 8 * hl;
-  const uint16_t *b = g.B + h * g.b_h + (int64_t)(n0 + l32) * g.K + 8 * hl;
-  constexpr int kC = 4;  // products (16 k) of a batch of loads
-  f32x16 acc = {};
-  u16x8 af[2][kC], bf[2][kC];
-  auto load = [&](int s, int k0) {
+  const int m0 = blockIdx.z * 32, n0 = blockIdx.x * 32, h = blockIdx.y;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), l32 = lane & 31, hl = lane >> 5;
+  const int m = m0 + l32, steps = g.K / 64, k0 = wave * steps * 16;
+  const uint16_t *a = g.A + (int64_t)min(m, g.M - 1) * g.a_m + h * g.a_h + k0 + 8 * hl;
+  const uint16_t *b = g.B + h * g.b_h + (int64_t)(n0 + l32) * g.K + k0 + 8 * hl;
+  constexpr int kMax = 8;  // K up to 512
+  u16x8 af[kMax], bf[kMax];
 #pragma unroll
-    for (int i = 0; i < kC; ++i) {
-      bf[s][i] = *reinterpret_cast<const u16x8 *>(b + k0 + 16 * i);
-      af[s][i] = *reinterpret_cast<const u16x8 *>(a + k0 + 16 * i);
+  for (int i = 0; i < kMax; ++i)
+    if (i < steps) {
+      bf[i] = *reinterpret_cast<const u16x8 *>(b + 16 * i);
+      af[i] = *reinterpret_cast<const u16x8 *>(a + 16 * i);
     }
-  };
-  load(0, 0);
-  for (int k0 = 0; k0 < g.K; k0 += 2 * 16 * kC) {
-    const bool two = k0 + 16 * kC < g.K;
-    if (two) load(1, k0 + 16 * kC);
+  const int M = g.hi ? min(g.M, *g.hi) : g.M, lo = g.lo ? *g.lo : 0;
+  f32x16 acc = {};
 #pragma unroll
-    for (int i = 0; i < kC; ++i) acc = E::mfma(bf[0][i], af[0][i], acc);
-    if (k0 + 2 * 16 * kC < g.K) load(0, k0 + 2 * 16 * kC);
-    if (two)
+  for (int i = 0; i < kMax; ++i)
+    if (i < steps) acc = E::mfma(bf[i], af[i], acc);
+  f32x4 *box = reinterpret_cast<f32x4 *>(lds);  // [wave][4 rows of c][lane]
 #pragma unroll
-      for (int i = 0; i < kC; ++i) acc = E::mfma(bf[1][i], af[1][i], acc);
+  for (int q = 0; q < 4; ++q)
+    box[(wave * 4 + q) * 64 + lane] = f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+  __syncthreads();
+  if (wave >= 2) return;
+  f32x4 sum[2];  // wave w: columns 16 w .. 16 w + 15
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    sum[q] = box[(2 * wave + q) * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) sum[q] += box[(w * 4 + 2 * wave + q) * 64 + lane];
   }
-  uint16_t *c = g.C + m * g.c_m + h * g.c_h + n0 + 8 * hl;
-#pragma unroll
-  for (int q = 0; q < 4; q += 2) {
-    const u32x4 v = rows8<E>(f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]},
-                             f32x4{acc[4 * q + 4], acc[4 * q + 5], acc[4 * q + 6], acc[4 * q + 7]});
-    if (m >= lo && m < M) *reinterpret_cast<u32x4 *>(c + 8 * q) = v;
-  }
+  const u32x4 v = rows8<E>(sum[0], sum[1]);
+  if (m >= lo && m < M)
+    *reinterpret_cast<u32x4 *>(g.C + m * g.c_m + h * g.c_h + n0 + 16 * wave + 8 * hl) = v;
 }
 
 // --- expanded keys and values: tiles of 256 rows x 256 columns ----------------------
@@ -320,8 +363,8 @@ __global__ __launch_bounds__(512, 1) void expand_gemm_kernel(ExpandGemm g) {
 template <typename E>
 void launch(moe_ctx *ctx, const HeadGemm &g, int H, const LatentPlan &p) {
   const unsigned extra = p.n_wg ? 1 : 0;  // a column of workgroups whose first makes the plan
-  if (g.M <= 64)
-    hipLaunchKernelGGL(head_gemm_stream_kernel<E>, dim3((g.N + 127) / 128 + extra, H, (g.M + 31) / 32), dim3(256), 0,
+  if (g.M <= 32)
+    hipLaunchKernelGGL(head_gemm_stream_kernel<E>, dim3(g.N / 32 + extra, H, (g.M + 31) / 32), dim3(256), 0,
                        ctx->stream, g, p);
   else if (g.N % 128 == 0)
     hipLaunchKernelGGL((head_gemm_tile_kernel<E, 128>), dim3((g.M + kBM - 1) / kBM * (g.N / 128) + extra, H), dim3(256),

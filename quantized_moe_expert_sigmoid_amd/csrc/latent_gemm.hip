@@ -277,85 +277,120 @@ __global__ __launch_bounds__(256) void head_gemm_stream_kernel(HeadGemm g, Laten
 }
 
 // --- expanded keys and values: tiles of 256 rows x 256 columns ----------------------
-// The heads' weights are one matrix of H N columns. Steps of 32 k: a row's 64
-// bytes of a step are 4 units of 16 in LDS, unit c at c ^ (row / 4) % 4 (16 rows'
-// equal units then lie in different banks). Four stages, one read while three are
-// in flight; 8 waves of 64 rows x 128 columns, two a SIMD.
+// The heads' weights are one matrix of H N columns. Steps of 64 k as above, two
+// stages; 8 waves of 64 rows x 128 columns, two a SIMD. K is short (2 to 8 steps),
+// so a workgroup goes on from tile to tile: the next tile's first step is loaded
+// under the last step's products, and a tile's stores drain under the next one's
+// products (with a tile a workgroup, which loads, multiplies and stores in turn,
+// 4096 rows of 128 heads of 256 columns took 181 us; KNOWN so).
 template <typename E>
 __global__ __launch_bounds__(512, 1) void expand_gemm_kernel(ExpandGemm g) {
-  constexpr int kStage = 512 * 64, kStages = 4, kLoads = 4;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages * kStage];
+  constexpr int kStage = 512 * 128, kLoads = 8, kStores = 16;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
   const int M = min(g.M, uniform(*g.hi)), cols = g.H * g.N;
   // an XCD (ids go round the 8 of them) takes whole column tiles, row tile by row tile
-  const int m_tiles = (g.M + 255) / 256, local = blockIdx.x >> 3;
-  const int m0 = local % m_tiles * 256, n0 = ((blockIdx.x & 7) + 8 * (local / m_tiles)) * 256;
-  if (m0 >= M || n0 >= cols) return;
+  const int xcd = blockIdx.x & 7, m_tiles = (M + 255) / 256, n_tiles = (cols + 255) / 256;
+  const int count = (n_tiles - xcd + 7) / 8 * m_tiles, stride = gridDim.x >> 3;
+  int t = blockIdx.x >> 3;
+  if (t >= count) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), l32 = lane & 31, hl = lane >> 5;
   const int wm = (wave & 3) * 64, wn = (wave >> 2) * 128;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
-  // loads: 16 rows x 64 bytes a wave and instruction; waves 0-3 rows, 4-7 columns (weights)
+  auto m_of = [&](int tile) { return tile % m_tiles * 256; };
+  auto n_of = [&](int tile) { return (xcd + 8 * (tile / m_tiles)) * 256; };
+  // loads: 8 rows x 128 bytes a wave and instruction; waves 0-3 rows, 4-7 columns (weights)
   const uint16_t *src[kLoads];
+  auto aim = [&](int tile) {
+    const int first = wave < 4 ? m_of(tile) : n_of(tile), last = (wave < 4 ? M : cols) - 1;
+    const uint16_t *base = wave < 4 ? g.A : g.B;
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int r = ((wave & 3) * kLoads + i) * 16 + (lane >> 2), unit = (lane & 3) ^ (r >> 2 & 3);
-    src[i] = (wave < 4 ? g.A + (int64_t)min(m0 + r, M - 1) * g.K : g.B + (int64_t)min(n0 + r, cols - 1) * g.K) + unit * 8;
-  }
-  auto load = [&](int i, int s) {
-    lds_load16<0>(src[i] + s * 32, uniform(lds0 + (s % kStages) * kStage + (wave * kLoads + i) * 1024),
-                  uniform(s * 32 < g.K ? -1 : 0));
-  };
-  f32x16 acc[4][2];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
-  int off[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) off[k] = l32 * 64 + (((2 * k + hl) ^ (l32 >> 2 & 3)) << 4);
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s)
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) load(i, s);
-  const int steps = g.K / 32;
-  for (int s = 0; s < steps; ++s) {
-    WAIT_VM((kStages - 2) * kLoads);
-    asm volatile("s_barrier" ::: "memory");
-    const uint8_t *as = lds + (s % kStages) * kStage + wm * 64, *bs = lds + (s % kStages) * kStage + (256 + wn) * 64;
-    u16x8 af[2][2], bf[2][4];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) af[k][j] = *reinterpret_cast<const u16x8 *>(as + j * 2048 + off[k]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) bf[k][i] = *reinterpret_cast<const u16x8 *>(bs + i * 2048 + off[k]);
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = ((wave & 3) * kLoads + i) * 8 + (lane >> 3), unit = (lane & 7) ^ swz(r & 15);
+      src[i] = base + (int64_t)min(first + r, last) * g.K + unit * 8;
     }
-    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto load = [&](int i, int s, int on) {
+    lds_load16<0>(src[i] + s * kBK, uniform(lds0 + (s & 1) * kStage + (wave * kLoads + i) * 1024), uniform(on));
+  };
+  int off[4];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+  for (int k = 0; k < 4; ++k) off[k] = l32 * 128 + (((2 * k + hl) ^ swz(l32 & 15)) << 4);
+  const int steps = g.K / kBK;  // even: a tile's first step goes to the stage that its predecessor's last one does not use
+  aim(t);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kLoads; ++i) load(i, 0, -1);
+  bool stores = false;  // the tile before has left exactly kStores stores behind this one's first loads
+  for (; t < count; t += stride) {
+    const int m0 = m_of(t), n0 = n_of(t);
+    f32x16 acc[4][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = E::mfma(bf[k][i], af[k][j], acc[i][j]);
-        if (i & 1) load(2 * k + (i >> 1), s + kStages - 1);
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+    for (int s = 0; s < steps; ++s) {
+      if (s == 0 && stores)
+        WAIT_VM(kStores);
+      else
+        WAIT_VM(0);
+      asm volatile("s_barrier" ::: "memory");
+      const uint8_t *as = lds + (s & 1) * kStage + wm * 128, *bs = lds + (s & 1) * kStage + (256 + wn) * 128;
+      u16x8 af[2][2], bf[2][4];
+      auto read = [&](int k) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) af[k & 1][j] = *reinterpret_cast<const u16x8 *>(as + j * 4096 + off[k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bf[k & 1][i] = *reinterpret_cast<const u16x8 *>(bs + i * 4096 + off[k]);
+      };
+      read(0);
+      const bool end = s + 1 == steps;
+      const int on = !end || t + stride < count ? -1 : 0, next = end ? 0 : s + 1;
+      if (end && on) aim(t + stride);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k < 3) read(k + 1);
         __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[i][j] = E::mfma(bf[k & 1][i], af[k & 1][j], acc[i][j]);
+          if (4 * k + i < kLoads) load(4 * k + i, next, on);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
-  }
+    }
+    auto place = [&](int i, int j) {
+      const int n = n0 + wn + 32 * i, h = n / g.N;
+      return g.C + ((int64_t)h * g.M + (m0 + wm + 32 * j + l32)) * g.N + (n - h * g.N) + 8 * hl;
+    };
+    auto value = [&](int i, int j, int q) {
+      const f32x16 &r = acc[i][j];
+      return rows8<E>(f32x4{r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]},
+                      f32x4{r[4 * q + 4], r[4 * q + 5], r[4 * q + 6], r[4 * q + 7]});
+    };
+    stores = m0 + 256 <= M && n0 + 256 <= cols;
+    if (stores) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = n0 + wn + 32 * i;
-    if (n >= cols) break;
-    const int h = n / g.N;
-    uint16_t *c = g.C + ((int64_t)h * g.M) * g.N + (n - h * g.N) + 8 * hl;
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int m = m0 + wm + 32 * j + l32;
+        for (int j = 0; j < 2; ++j) {
+          uint16_t *c = place(i, j);
+          *reinterpret_cast<u32x4 *>(c) = value(i, j, 0);
+          *reinterpret_cast<u32x4 *>(c + 16) = value(i, j, 2);
+        }
+    } else {
 #pragma unroll
-      for (int q = 0; q < 4; q += 2) {
-        const f32x16 &r = acc[i][j];
-        const u32x4 v = rows8<E>(f32x4{r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]},
-                                 f32x4{r[4 * q + 4], r[4 * q + 5], r[4 * q + 6], r[4 * q + 7]});
-        if (m < M) *reinterpret_cast<u32x4 *>(c + (int64_t)m * g.N + 8 * q) = v;
-      }
+      for (int i = 0; i < 4; ++i)
+        if (n0 + wn + 32 * i < cols)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint16_t *c = place(i, j);
+            const u32x4 v0 = value(i, j, 0), v1 = value(i, j, 2);
+            if (m0 + wm + 32 * j + l32 < M) {
+              *reinterpret_cast<u32x4 *>(c) = v0;
+              *reinterpret_cast<u32x4 *>(c + 16) = v1;
+            }
+          }
     }
   }
 }
@@ -386,8 +421,7 @@ moe_status launch_head_gemm(moe_ctx *ctx, int dtype, const HeadGemm &g, int H, c
 }
 
 moe_status launch_expand_gemm(moe_ctx *ctx, int dtype, const ExpandGemm &g) {
-  const unsigned m_tiles = (g.M + 255) / 256, n_tiles = (g.H * g.N + 255) / 256;
-  const dim3 grid(m_tiles * ((n_tiles + 7) / 8) * 8);
+  const dim3 grid(ctx->n_cu / 8 * 8);
   if (dtype == MOE_BF16)
     hipLaunchKernelGGL(expand_gemm_kernel<Bf16>, grid, dim3(512), 0, ctx->stream, g);
   else

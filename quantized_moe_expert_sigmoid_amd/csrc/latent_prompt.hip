@@ -31,46 +31,95 @@ struct PromptWs {
   int64_t n_kv;
 };
 
-__global__ __launch_bounds__(1024) void prompt_plan_kernel(LatentArgs a, PromptWs ws) {
-  __shared__ int scan[1024], tiles[1024];
-  const int b = threadIdx.x;
-  const LatentSeq s = b < a.B ? latent_seq(a, b) : LatentSeq{};
-  const int nt = (s.nq + kRows - 1) / kRows;
-  scan[b] = s.len;
-  tiles[b] = nt;
-  __syncthreads();
-  for (int o = 1; o < 1024; o <<= 1) {
-    const int v = b >= o ? scan[b - o] : 0, t = b >= o ? tiles[b - o] : 0;
-    __syncthreads();
-    scan[b] = (int)min((int64_t)scan[b] + v, (int64_t)1 << 30);  // a total that saturates is above n_kv anyway
-    tiles[b] += t;
-    __syncthreads();
-  }
-  if (b < a.B) {
-    const bool fits = scan[b] <= ws.n_kv;
-    if (!fits) atomicOr(a.err, (uint32_t)ERRF_LATENT);
-    ws.off[b] = fits ? scan[b] - s.len : -1;
-    for (int i = 0; i < nt; ++i) ws.tile[tiles[b] - nt + i] = PromptTile{b, i * kRows};
-    // the last sequence that fits ends the expanded rows
-    if (fits && (b + 1 == a.B || scan[b + 1] > ws.n_kv)) ws.off[a.B] = scan[b];
-    if (!fits && b == 0) ws.off[a.B] = 0;
-  }
-  if (b == 1023) *ws.n_tiles = tiles[b];
-}
-
-// The sequences' cache rows one after another: a wave a row, 16 bytes a lane
-// (the rotary part by the first lanes again).
+// The sequences' cache rows one after another (a wave a row, 16 bytes a lane, the
+// rotary part by the first lanes again). Every workgroup sums the lengths by
+// itself; the first one also writes the plan: row tiles by falling number of
+// tokens they see, so that the workgroups that take them end together.
 __global__ __launch_bounds__(256) void prompt_rows_kernel(LatentArgs a, PromptWs ws) {
-  const int b = blockIdx.y, off = ws.off[b], lane = threadIdx.x & 63;
-  if (off < 0) return;
-  const LatentSeq s = latent_seq(a, b);
-  for (int j = blockIdx.x * 4 + (threadIdx.x >> 6); j < s.len; j += gridDim.x * 4) {
-    const uint16_t *row = static_cast<const uint16_t *>(a.cache) + latent_row(a, b, j) * (a.dc + a.dr) + 8 * lane;
-    if (8 * lane < a.dc)
-      *reinterpret_cast<u32x4 *>(ws.c + (int64_t)(off + j) * a.dc + 8 * lane) = *reinterpret_cast<const u32x4 *>(row);
-    if (8 * lane < a.dr)
-      *reinterpret_cast<u32x4 *>(ws.kr + (int64_t)(off + j) * a.dr + 8 * lane) =
-          *reinterpret_cast<const u32x4 *>(row + a.dc);
+  constexpr int kPer = 4;  // sequences a thread
+  constexpr int kSort = 256;
+  __shared__ int off_s[1024], tmp[8], sees[kSort];
+  __shared__ PromptTile tile_s[kSort];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const bool first = blockIdx.x == 0;
+  int len[kPer], nt[kPer], nq[kPer], sum = 0, tsum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = tid * kPer + i;
+    const LatentSeq s = b < a.B ? latent_seq(a, b) : LatentSeq{};
+    len[i] = s.len;
+    nq[i] = s.nq;
+    nt[i] = (s.nq + kRows - 1) / kRows;
+    sum = (int)min((int64_t)sum + len[i], (int64_t)1 << 30);  // a total that saturates is above n_kv anyway
+    tsum += nt[i];
+  }
+  int at = sum, tat = tsum;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int x = __shfl_up(at, o, 64), y = __shfl_up(tat, o, 64);
+    at = lane >= o ? (int)min((int64_t)at + x, (int64_t)1 << 30) : at;
+    tat += lane >= o ? y : 0;
+  }
+  if (lane == 63) {
+    tmp[wave] = at;
+    tmp[4 + wave] = tat;
+  }
+  __syncthreads();
+  int64_t before = 0;
+  int tbefore = 0, n_tiles = 0;
+  for (int w = 0; w < 4; ++w) {
+    before += w < wave ? tmp[w] : 0;
+    tbefore += w < wave ? tmp[4 + w] : 0;
+    n_tiles += tmp[4 + w];
+  }
+  int64_t o = before + at - sum;
+  int t = tbefore + tat - tsum;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = tid * kPer + i;
+    const bool fits = o + len[i] <= ws.n_kv;
+    off_s[b] = fits ? (int)o : -1;
+    if (first && b < a.B) {
+      if (!fits) atomicOr(a.err, (uint32_t)ERRF_LATENT);
+      ws.off[b] = fits ? (int)o : -1;
+      if (n_tiles > kSort)
+        for (int k = 0; k < nt[i]; ++k) ws.tile[t + k] = PromptTile{b, k * kRows};
+      else
+        for (int k = 0; k < nt[i]; ++k) {
+          tile_s[t + k] = PromptTile{b, k * kRows};
+          sees[t + k] = max(0, min(len[i], len[i] - nq[i] + min(nq[i], (k + 1) * kRows)));
+        }
+      // the last sequence that fits ends the expanded rows
+      if (fits && b + 1 == a.B) ws.off[a.B] = (int)(o + len[i]);
+      if (!fits && o <= ws.n_kv) ws.off[a.B] = (int)o;
+    }
+    o += len[i];
+    t += nt[i];
+  }
+  if (first && tid == 0) *ws.n_tiles = n_tiles;
+  __syncthreads();
+  if (first && n_tiles <= kSort && tid < n_tiles) {
+    const int mine = sees[tid];
+    int rank = 0;
+    for (int x = 0; x < n_tiles; ++x) rank += sees[x] > mine || (sees[x] == mine && x < tid);
+    ws.tile[rank] = tile_s[tid];
+  }
+  // rows, spread over all workgroups
+  for (int b = 0; b < a.B; ++b) {
+    const int off = off_s[b], n = (b + 1 < 1024 && off_s[b + 1] >= 0 && b + 1 < a.B) ? off_s[b + 1] - off : -1;
+    if (off < 0) continue;
+    const int rows = n >= 0 ? n : latent_seq(a, b).len;
+    const uint16_t *cache = static_cast<const uint16_t *>(a.cache) + 8 * lane;
+    // workgroup and wave take rows off + j = id (mod all), so that short sequences use different ones
+    const int all = gridDim.x * 4, id = blockIdx.x * 4 + wave;
+    for (int j = (id - off % all + all) % all; j < rows; j += all) {
+      const uint16_t *row = cache + latent_row(a, b, j) * (a.dc + a.dr);
+      if (8 * lane < a.dc)
+        *reinterpret_cast<u32x4 *>(ws.c + (int64_t)(off + j) * a.dc + 8 * lane) = *reinterpret_cast<const u32x4 *>(row);
+      if (8 * lane < a.dr)
+        *reinterpret_cast<u32x4 *>(ws.kr + (int64_t)(off + j) * a.dr + 8 * lane) =
+            *reinterpret_cast<const u32x4 *>(row + a.dc);
+    }
   }
 }
 
@@ -92,12 +141,12 @@ __global__ __launch_bounds__(512, 1) void latent_prompt_kernel(LatentArgs a, Pro
   using C = Prompt<DN, DR, DV>;
   constexpr int kNT = C::kNT, kTB = C::kTB, kNB = C::kNB, DX = DN + DV, kAhead = 4;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kBufs * C::kTileB];
-  // an XCD (ids go round the 8 of them) takes whole heads, so that workgroups that share keys share an L2; late
-  // tiles, which see the most, go first
-  const int nt = uniform(*ws.n_tiles), id = blockIdx.x >> 3;
-  const int h = (blockIdx.x & 7) + 8 * (id / max(nt, 1));
-  if (nt == 0 || h >= a.H) return;
-  const PromptTile pt = ws.tile[nt - 1 - id % nt];
+  // an XCD (ids go round the 8 of them) takes whole heads, so that workgroups that share keys share an L2; the tiles
+  // that see the most go first, of all its heads (head by head left 23% of the CUs' time at the end idle)
+  const int nt = uniform(*ws.n_tiles), per_xcd = (a.H + 7) / 8, id = blockIdx.x >> 3;
+  const int h = (blockIdx.x & 7) + 8 * (id % per_xcd);
+  if (id / per_xcd >= nt || h >= a.H) return;
+  const PromptTile pt = ws.tile[id / per_xcd];
   const int b = uniform(pt.b), i0 = uniform(pt.i0), off0 = uniform(ws.off[b]);
   if (off0 < 0) return;
   const LatentSeq r = latent_seq(a, b);
@@ -331,12 +380,10 @@ moe_status launch(moe_ctx *ctx, const LatentArgs &a, int64_t n_kv) {
                     reinterpret_cast<PromptTile *>(p + o_tile), reinterpret_cast<uint16_t *>(p + o_c),
                     reinterpret_cast<uint16_t *>(p + o_kr),  reinterpret_cast<uint16_t *>(p + o_x),
                     n_kv};
-  hipLaunchKernelGGL(prompt_plan_kernel, dim3(1), dim3(1024), 0, ctx->stream, a, ws);
-  MOE_CHECK_LAUNCH("prompt_plan_kernel");
+  const unsigned row_blocks = (unsigned)std::max<int64_t>(1, std::min<int64_t>((n_kv + 3) / 4, 1024));
+  hipLaunchKernelGGL(prompt_rows_kernel, dim3(row_blocks), dim3(256), 0, ctx->stream, a, ws);
+  MOE_CHECK_LAUNCH("prompt_rows_kernel");
   if (n_kv > 0) {
-    const unsigned row_blocks = (unsigned)std::max<int64_t>(1, std::min<int64_t>(n_kv / 4, 2048) / a.B);
-    hipLaunchKernelGGL(prompt_rows_kernel, dim3(row_blocks, a.B), dim3(256), 0, ctx->stream, a, ws);
-    MOE_CHECK_LAUNCH("prompt_rows_kernel");
     const ExpandGemm expand{ws.c, static_cast<const uint16_t *>(a.w_kv), ws.x, ws.off + a.B, (int)n_kv, a.H, DN + DV,
                             a.dc};
     if ((st = launch_expand_gemm(ctx, E::kDtype, expand))) return st;

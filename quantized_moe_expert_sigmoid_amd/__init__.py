@@ -137,6 +137,8 @@ def exported_names():
 def lib():
     """Load libmoe.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -169,7 +171,7 @@ def _dev(t: torch.Tensor, dtype, name, shape=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
     return t.data_ptr()
 
@@ -475,6 +477,7 @@ class LatentCfg:
         self.struct = _LatentCfg(n_heads, d_latent, d_rope, d_nope, d_v, 0 if dtype == torch.bfloat16 else 1,
                                  page_size, self.scale)
         self.ref = ctypes.byref(self.struct)
+        self.row = d_latent + d_rope  # elements of a cached row
 
 
 def _rows3(t: torch.Tensor, dtype, name, shape):
@@ -499,44 +502,42 @@ def moe_latent_append(ctx: MoeCtx, cfg: LatentCfg, kv: torch.Tensor, turn: torch
     + d_rope] (rows may be strided), turn fp32 [n_pos][d_rope/2][2], pos int32
     [T], slot int64 [T] (-1: not kept), cache [n_pages][page][d_latent + d_rope];
     q_rope [T][H][d_rope] (a strided view is fine) is rotated into q_rope_out."""
-    T, row = kv.shape[0], cfg.d_latent + cfg.d_rope
-    if not kv.is_cuda or kv.dtype != cfg.dtype:
-        raise TypeError(f"kv must be a CUDA (HIP) {cfg.dtype} tensor")
+    T, row, dtype = kv.shape[0], cfg.row, cfg.dtype
+    if not kv.is_cuda or kv.dtype != dtype:
+        raise TypeError(f"kv must be a CUDA (HIP) {dtype} tensor")
     if kv.shape != (T, row) or kv.stride(1) != 1:
         raise ValueError(f"kv must be [T][{row}] with contiguous rows")
-    _dev(turn, torch.float32, "turn", (turn.shape[0], cfg.d_rope // 2, 2))
-    _dev(pos, torch.int32, "pos", (T,))
-    _dev(slot, torch.int64, "slot", (T,))
-    _dev(cache, cfg.dtype, "cache", (cache.shape[0], cfg.page_size, row))
-    if norm_w is not None:
-        _dev(norm_w, torch.float32, "norm_w", (cfg.d_latent,))
-    qr, qt, qh = None, 0, 0
+    n_pos, n_pages = turn.shape[0], cache.shape[0]
+    turn_p = _dev(turn, torch.float32, "turn", (n_pos, cfg.d_rope // 2, 2))
+    pos_p = _dev(pos, torch.int32, "pos", (T,))
+    slot_p = _dev(slot, torch.int64, "slot", (T,))
+    cache_p = _dev(cache, dtype, "cache", (n_pages, cfg.page_size, row))
+    norm_p = None if norm_w is None else _dev(norm_w, torch.float32, "norm_w", (cfg.d_latent,))
+    qr, qt, qh, out_p = None, 0, 0, None
     if q_rope is not None:
         shape = (T, cfg.n_heads, cfg.d_rope)
-        qr, qt, qh = _rows3(q_rope, cfg.dtype, "q_rope", shape)
+        qr, qt, qh = _rows3(q_rope, dtype, "q_rope", shape)
         if q_rope_out is None:
             raise ValueError("q_rope needs q_rope_out")
-        _dev(q_rope_out, cfg.dtype, "q_rope_out", shape)
+        out_p = _dev(q_rope_out, dtype, "q_rope_out", shape)
     elif q_rope_out is not None:
         raise ValueError("q_rope_out needs q_rope")
-    _ck(lib().moe_latent_append(ctx.handle, cfg.ref, T, kv.data_ptr(), kv.stride(0) if T > 1 else row, _ptr(norm_w),
-                                eps, turn.data_ptr(), turn.shape[0], pos.data_ptr(), slot.data_ptr(),
-                                cache.data_ptr(), cache.shape[0], qr, qt, qh, _ptr(q_rope_out)))
+    _ck(lib().moe_latent_append(ctx.handle, cfg.ref, T, kv.data_ptr(), kv.stride(0) if T > 1 else row, norm_p, eps,
+                                turn_p, n_pos, pos_p, slot_p, cache_p, n_pages, qr, qt, qh, out_p))
     return cache
 
 
 def _latent_call(cfg, q_nope, q_rope, w_kv, cache, table, q_start, kv_len, out):
-    T, B, H = q_nope.shape[0], kv_len.shape[0], cfg.n_heads
-    qn, nt, nh = _rows3(q_nope, cfg.dtype, "q_nope", (T, H, cfg.d_nope))
-    qr, rt, rh = _rows3(q_rope, cfg.dtype, "q_rope", (T, H, cfg.d_rope))
-    _dev(w_kv, cfg.dtype, "w_kv", (H, cfg.d_nope + cfg.d_v, cfg.d_latent))
-    _dev(cache, cfg.dtype, "cache", (cache.shape[0], cfg.page_size, cfg.d_latent + cfg.d_rope))
-    _dev(table, torch.int32, "table", (B, table.shape[1]))
-    _dev(q_start, torch.int32, "q_start", (B + 1,))
-    _dev(kv_len, torch.int32, "kv_len", (B,))
-    _dev(out, cfg.dtype, "out", (T, H, cfg.d_v))
-    return _LatentCall(T, B, qn, nt, nh, qr, rt, rh, cache.data_ptr(), cache.shape[0], table.data_ptr(),
-                       table.shape[1], q_start.data_ptr(), kv_len.data_ptr(), out.data_ptr())
+    T, B, H, dtype = q_nope.shape[0], kv_len.shape[0], cfg.n_heads, cfg.dtype
+    qn, nt, nh = _rows3(q_nope, dtype, "q_nope", (T, H, cfg.d_nope))
+    qr, rt, rh = _rows3(q_rope, dtype, "q_rope", (T, H, cfg.d_rope))
+    n_pages, max_pages = cache.shape[0], table.shape[1]
+    w_p = _dev(w_kv, dtype, "w_kv", (H, cfg.d_nope + cfg.d_v, cfg.d_latent))
+    return _LatentCall(T, B, qn, nt, nh, qr, rt, rh,
+                       _dev(cache, dtype, "cache", (n_pages, cfg.page_size, cfg.row)), n_pages,
+                       _dev(table, torch.int32, "table", (B, max_pages)), max_pages,
+                       _dev(q_start, torch.int32, "q_start", (B + 1,)), _dev(kv_len, torch.int32, "kv_len", (B,)),
+                       _dev(out, dtype, "out", (T, H, cfg.d_v))), w_p
 
 
 def moe_latent_attend(ctx: MoeCtx, cfg: LatentCfg, q_nope: torch.Tensor, q_rope: torch.Tensor, w_kt: torch.Tensor,
@@ -546,13 +547,12 @@ def moe_latent_attend(ctx: MoeCtx, cfg: LatentCfg, q_nope: torch.Tensor, q_rope:
     [T][H][d_nope] and q_rope [T][H][d_rope] (strided views are fine), w_kt
     [H][d_latent][d_nope], w_kv [H][d_nope + d_v][d_latent], table int32
     [B][max_pages], q_start int32 [B+1], kv_len int32 [B], out [T][H][d_v];
-    tree: int64 [T], each token's visible own rows as bits (NULL: causal)."""
-    call = _latent_call(cfg, q_nope, q_rope, w_kv, cache, table, q_start, kv_len, out)
-    _dev(w_kt, cfg.dtype, "w_kt", (cfg.n_heads, cfg.d_latent, cfg.d_nope))
-    if tree is not None:
-        _dev(tree, torch.int64, "tree", (call.T,))
-    _ck(lib().moe_latent_attend(ctx.handle, cfg.ref, ctypes.byref(call), w_kt.data_ptr(), w_kv.data_ptr(),
-                                _ptr(tree), max_q))
+    tree: int64 [T], each token's visible own rows as bits (None: causal)."""
+    call, w_p = _latent_call(cfg, q_nope, q_rope, w_kv, cache, table, q_start, kv_len, out)
+    t_p = None if tree is None else _dev(tree, torch.int64, "tree", (call.T,))
+    _ck(lib().moe_latent_attend(ctx.handle, cfg.ref, ctypes.byref(call),
+                                _dev(w_kt, cfg.dtype, "w_kt", (cfg.n_heads, cfg.d_latent, cfg.d_nope)), w_p, t_p,
+                                max_q))
     return out
 
 
@@ -561,8 +561,8 @@ def moe_latent_prompt(ctx: MoeCtx, cfg: LatentCfg, q_nope: torch.Tensor, q_rope:
                       n_kv: int, out: torch.Tensor):
     """Expanded form, causal (see include/moe.h): arguments as for
     moe_latent_attend; n_kv: at least the sum of kv_len."""
-    call = _latent_call(cfg, q_nope, q_rope, w_kv, cache, table, q_start, kv_len, out)
-    _ck(lib().moe_latent_prompt(ctx.handle, cfg.ref, ctypes.byref(call), w_kv.data_ptr(), n_kv))
+    call, w_p = _latent_call(cfg, q_nope, q_rope, w_kv, cache, table, q_start, kv_len, out)
+    _ck(lib().moe_latent_prompt(ctx.handle, cfg.ref, ctypes.byref(call), w_p, n_kv))
     return out
 
 

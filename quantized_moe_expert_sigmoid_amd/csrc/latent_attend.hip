@@ -82,6 +82,7 @@ __global__ __launch_bounds__(256, (Attend<DC, DR, WM, WN>::kPerCu)) void latent_
   using C = Attend<DC, DR, WM, WN>;
   constexpr int kNB = C::kNB, kBufs = C::kBufs, kPanels = C::kPanels, kAhead = C::kPerCu == 2 ? 4 : 6, kChains = 2;
   constexpr int kLoadStep = (C::kKS - 4) / kPanels;  // a panel's load every so many products
+  static_assert(kLoadStep >= 1, "every load has its place");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLds];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN, l32 = lane & 31, hl = lane >> 5;
@@ -428,7 +429,7 @@ __global__ __launch_bounds__(256) void latent_merge_kernel(LatentArgs a, AttendW
   }
   float m = -__builtin_inff(), l = 0.0f;
   f32x4 acc[J] = {};
-  constexpr int kB = 8 / J == 8 ? 4 : 1;  // partial results read at a time
+  constexpr int kB = J == 1 ? 8 : 1;  // partial results read at a time
   for (int i = wave; i < n; i += 4 * kB) {
     float2 ml[kB];
     f32x4 v[kB][J];

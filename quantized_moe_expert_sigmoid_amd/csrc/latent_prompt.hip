@@ -3,8 +3,8 @@
 //
 // As in the absorbed form a lane keeps one query row: S^T = K Q^T, P^T, O^T +=
 // V^T P^T with v_mfma_f32_32x32x16 (see latent_attend.hip for the layouts). A
-// workgroup takes 256 tokens of one head, 32 a wave, two waves a SIMD, so that
-// one wave's exponentials run under the other's products; its tiles of keys and
+// workgroup takes 256 (or 128) tokens of one head, 32 a wave, two waves a SIMD, so
+// that one wave's exponentials run under the other's products; its tiles of keys and
 // values come into LDS by asynchronous loads, one being read, the others in
 // flight.
 #include "latent.h"
@@ -13,7 +13,6 @@
 
 namespace {
 
-constexpr int kRows = 256;  // query tokens of a workgroup
 
 // The plan: off[b] = first expanded row of sequence b (B + 1 entries), the
 // row tiles. Sequences that do not fit n_kv rows are
@@ -29,6 +28,7 @@ struct PromptWs {
   uint16_t *kr;      // [n_kv][dr] rotary keys
   uint16_t *x;       // [H][n_kv][dn + dv] keys and values
   int64_t n_kv;
+  int tile_rows;     // query tokens of a row tile
 };
 
 // The sequences' cache rows one after another (a wave a row, 16 bytes a lane, the
@@ -49,7 +49,7 @@ __global__ __launch_bounds__(256) void prompt_rows_kernel(LatentArgs a, PromptWs
     const LatentSeq s = b < a.B ? latent_seq(a, b) : LatentSeq{};
     len[i] = s.len;
     nq[i] = s.nq;
-    nt[i] = (s.nq + kRows - 1) / kRows;
+    nt[i] = (s.nq + ws.tile_rows - 1) / ws.tile_rows;
     sum = (int)min((int64_t)sum + len[i], (int64_t)1 << 30);  // a total that saturates is above n_kv anyway
     tsum += nt[i];
   }
@@ -83,11 +83,11 @@ __global__ __launch_bounds__(256) void prompt_rows_kernel(LatentArgs a, PromptWs
       if (!fits) atomicOr(a.err, (uint32_t)ERRF_LATENT);
       ws.off[b] = fits ? (int)o : -1;
       if (n_tiles > kSort)
-        for (int k = 0; k < nt[i]; ++k) ws.tile[t + k] = PromptTile{b, k * kRows};
+        for (int k = 0; k < nt[i]; ++k) ws.tile[t + k] = PromptTile{b, k * ws.tile_rows};
       else
         for (int k = 0; k < nt[i]; ++k) {
-          tile_s[t + k] = PromptTile{b, k * kRows};
-          sees[t + k] = max(0, min(len[i], len[i] - nq[i] + min(nq[i], (k + 1) * kRows)));
+          tile_s[t + k] = PromptTile{b, k * ws.tile_rows};
+          sees[t + k] = max(0, min(len[i], len[i] - nq[i] + min(nq[i], (k + 1) * ws.tile_rows)));
         }
       // the last sequence that fits ends the expanded rows
       if (fits && b + 1 == a.B) ws.off[a.B] = (int)(o + len[i]);
@@ -125,20 +125,23 @@ __global__ __launch_bounds__(256) void prompt_rows_kernel(LatentArgs a, PromptWs
 
 __device__ __forceinline__ int swz(int token) { return ((token >> 1 & 1) << 2) | (token >> 2 & 3); }
 
-template <int DN, int DR, int DV>
+template <int DN, int DR, int DV, int W>
 struct Prompt {
-  static constexpr int kTB = DV > 128 ? 1 : 2, kNT = 32 * kTB;  // 32 or 64 tokens a tile
+  static constexpr int kTB = DV > 128 || W == 4 ? 1 : 2, kNT = 32 * kTB;  // 32 or 64 tokens a tile
   static constexpr int kPN = DN / 64, kPK = kPN + 1, kPV = DV / 64;  // panels of 64 columns: keys (rotary part last), values
   static constexpr int kPanelB = kNT * 128, kTileB = (kPK + kPV) * kPanelB;
   static constexpr int kBufs = 3;
-  static constexpr int kLoads = (kPK + kPV) * kNT / 64;  // of a wave and tile
+  static constexpr int kLoads = (kPK + kPV) * kNT / 8 / W;  // of a wave and tile
+  static constexpr int kStep = W * 8 / kNT;                // waves that share a block of 8 tokens
   static constexpr int kKS = (DN + DR) / 16, kNB = DV / 32;
-  static_assert(kBufs * kTileB <= 160 << 10 && (kPK + kPV) * kNT % 64 == 0, "");
+  static_assert(kBufs * kTileB <= 160 << 10 && (kPK + kPV) % kStep == 0, "");
 };
 
-template <typename E, int DN, int DR, int DV>
-__global__ __launch_bounds__(512, 1) void latent_prompt_kernel(LatentArgs a, PromptWs ws, float c2, uint32_t flip) {
-  using C = Prompt<DN, DR, DV>;
+template <typename E, int DN, int DR, int DV, int W>
+__global__ __launch_bounds__(64 * W, W / 4) void latent_prompt_kernel(LatentArgs a, PromptWs ws, float c2,
+                                                                      uint32_t flip) {
+  using C = Prompt<DN, DR, DV, W>;
+  constexpr int kRows = 32 * W;
   constexpr int kNT = C::kNT, kTB = C::kTB, kNB = C::kNB, DX = DN + DV, kAhead = 4;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kBufs * C::kTileB];
   // an XCD (ids go round the 8 of them) takes whole heads, so that workgroups that share keys share an L2; the tiles
@@ -192,7 +195,7 @@ __global__ __launch_bounds__(512, 1) void latent_prompt_kernel(LatentArgs a, Pro
     on = uniform(i < n ? -1 : 0);
   };
   // panels: keys, rotary keys, values; with tiles of 32 tokens two waves share a block of 8 and take every other one
-  constexpr int kStep = 64 / kNT;
+  constexpr int kStep = C::kStep;
   const int odd_wave = kStep == 1 ? 0 : uniform(wave >> 2);
   auto load = [&](auto i) {
     constexpr int g = i * kStep;
@@ -242,6 +245,8 @@ __global__ __launch_bounds__(512, 1) void latent_prompt_kernel(LatentArgs a, Pro
     // Operands are read kAhead products before they are used, the next tile's loads go in between, and the order is
     // held (see latent_attend.hip).
     constexpr int kZ = C::kKS * kTB, kV = 2 * kTB * kNB;  // products
+    constexpr int kEvery = kZ >= 2 * C::kLoads ? 2 : 1;
+    static_assert(kZ / kEvery >= C::kLoads, "every load has its place");
     auto k_read = [&](int i) {
       const int k = i / kTB, tb = i % kTB;
       return *reinterpret_cast<const u16x8 *>(kv + k_off[k & 3] + (k >> 2) * C::kPanelB + tb * 32 * 128);
@@ -265,7 +270,7 @@ __global__ __launch_bounds__(512, 1) void latent_prompt_kernel(LatentArgs a, Pro
         ring[i % kAhead] = k_read(i + kAhead);
       else if (i + kAhead - kZ < kV)
         ring[i % kAhead] = v_read(i + kAhead - kZ);
-      if constexpr (i % 2 == 1 && i / 2 < C::kLoads) load(std::integral_constant<int, i / 2>{});
+      if constexpr (i % kEvery == kEvery - 1 && i / kEvery < C::kLoads) load(std::integral_constant<int, i / kEvery>{});
       __builtin_amdgcn_sched_barrier(0);
     });
     if (masked) {
@@ -298,7 +303,7 @@ __global__ __launch_bounds__(512, 1) void latent_prompt_kernel(LatentArgs a, Pro
         __syncthreads();
         if (broken)
 #pragma unroll 1
-          for (int c = wave; c < DV / 8; c += 8)
+          for (int c = wave; c < DV / 8; c += W)
             *reinterpret_cast<u32x4 *>(vv + (c >> 3) * C::kPanelB + row * 128 + (((c & 7) ^ swz(row & 15)) << 4)) =
                 u32x4{0, 0, 0, 0};
 #pragma unroll
@@ -365,8 +370,9 @@ __global__ __launch_bounds__(512, 1) void latent_prompt_kernel(LatentArgs a, Pro
     }
 }
 
-template <typename E, int DN, int DR, int DV>
+template <typename E, int DN, int DR, int DV, int W>
 moe_status launch(moe_ctx *ctx, const LatentArgs &a, int64_t n_kv) {
+  constexpr int kRows = 32 * W;
   const int64_t tiles = a.T / kRows + a.B;  // at most: every sequence adds one tile that is not full
   MoeLayout lay;
   const size_t o_off = lay.take(4 * (size_t)(a.B + 1)), o_nt = lay.take(4), o_tile = lay.take(sizeof(PromptTile) * tiles),
@@ -379,7 +385,8 @@ moe_status launch(moe_ctx *ctx, const LatentArgs &a, int64_t n_kv) {
   const PromptWs ws{reinterpret_cast<int32_t *>(p + o_off),  reinterpret_cast<int32_t *>(p + o_nt),
                     reinterpret_cast<PromptTile *>(p + o_tile), reinterpret_cast<uint16_t *>(p + o_c),
                     reinterpret_cast<uint16_t *>(p + o_kr),  reinterpret_cast<uint16_t *>(p + o_x),
-                    n_kv};
+                    n_kv,
+                    kRows};
   const unsigned row_blocks = (unsigned)std::max<int64_t>(1, std::min<int64_t>((n_kv + 3) / 4, 1024));
   hipLaunchKernelGGL(prompt_rows_kernel, dim3(row_blocks), dim3(256), 0, ctx->stream, a, ws);
   MOE_CHECK_LAUNCH("prompt_rows_kernel");
@@ -389,7 +396,7 @@ moe_status launch(moe_ctx *ctx, const LatentArgs &a, int64_t n_kv) {
     if ((st = launch_expand_gemm(ctx, E::kDtype, expand))) return st;
   }
   const float c2 = latent_c2(a.scale);
-  hipLaunchKernelGGL((latent_prompt_kernel<E, DN, DR, DV>), dim3((unsigned)(tiles * ((a.H + 7) / 8) * 8)), dim3(512), 0,
+  hipLaunchKernelGGL((latent_prompt_kernel<E, DN, DR, DV, W>), dim3((unsigned)(tiles * ((a.H + 7) / 8) * 8)), dim3(64 * W), 0,
                      ctx->stream, a, ws, c2, a.scale < 0 ? 0x80008000u : 0u);
   MOE_CHECK_LAUNCH("latent_prompt_kernel");
   return MOE_OK;
@@ -397,9 +404,14 @@ moe_status launch(moe_ctx *ctx, const LatentArgs &a, int64_t n_kv) {
 
 template <typename E, int DR>
 moe_status pick(moe_ctx *ctx, const LatentArgs &a, int64_t n_kv) {
-  return a.dn == 64    ? launch<E, 64, DR, 64>(ctx, a, n_kv)
-         : a.dn == 128 ? launch<E, 128, DR, 128>(ctx, a, n_kv)
-                       : launch<E, 192, DR, 256>(ctx, a, n_kv);
+  // row tiles of 256 tokens read keys and values half as often; of 128 where those would leave CUs without work
+  if ((a.T + 255) / 256 * (int64_t)a.H > ctx->n_cu)
+    return a.dn == 64    ? launch<E, 64, DR, 64, 8>(ctx, a, n_kv)
+           : a.dn == 128 ? launch<E, 128, DR, 128, 8>(ctx, a, n_kv)
+                         : launch<E, 192, DR, 256, 8>(ctx, a, n_kv);
+  return a.dn == 64    ? launch<E, 64, DR, 64, 4>(ctx, a, n_kv)
+         : a.dn == 128 ? launch<E, 128, DR, 128, 4>(ctx, a, n_kv)
+                       : launch<E, 192, DR, 256, 4>(ctx, a, n_kv);
 }
 
 }  // namespace

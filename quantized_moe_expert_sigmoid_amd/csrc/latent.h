@@ -49,8 +49,9 @@ struct alignas(32) WgDesc {
   int t0, nq, len, over;  // the sequence's bounds; units a row tile has ahead of its cache tiles
 };
 struct TileDesc {
-  int b, mt, w0, w1;  // a row tile whose cache tiles several workgroups share, and those
-  int64_t u0;         // its first unit
+  int b, mt, w0, n;  // a row tile whose cache tiles n workgroups share: w0, w0 + step, ..
+  int step;
+  int64_t u0;        // its first unit
 };
 struct PlanHead {
   int64_t per;   // units of a workgroup

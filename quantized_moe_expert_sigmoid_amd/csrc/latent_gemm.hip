@@ -68,17 +68,20 @@ __device__ void make_plan(const LatentPlan &p, uint8_t *lds) {
   int64_t total, n_rows;
   scan_excl<int64_t>(u, tmp, total);
   scan_excl<int64_t>(rt, tmp, n_rows);
-  const int64_t even = (total + p.n_wg - 1) / p.n_wg;
+  auto div_up = [](int64_t x, int64_t y) {  // 64-bit division is slow, and rarely needed
+    return x + y < (1ll << 31) ? (int64_t)(((uint32_t)x + (uint32_t)y - 1) / (uint32_t)y) : (x + y - 1) / y;
+  };
+  const int64_t even = div_up(total, p.n_wg);
 
   // the smallest pieces that are no more than the workgroups
   int piece = 0;
   if (n_rows > 0 && n_rows < p.n_wg) {
-    int64_t lo = even, hi = min(even + p.over, (total + p.n_wg - n_rows - 1) / (p.n_wg - n_rows));
+    int64_t lo = even, hi = min(even + p.over, div_up(total, p.n_wg - n_rows));
     while (lo <= hi) {
       const int64_t mid = (lo + hi) >> 1;
       int64_t c = 0, n;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) c += (int64_t)rr[i] * ((kk[i] + mid - 1) / mid);
+      for (int i = 0; i < kPer; ++i) c += (int64_t)rr[i] * div_up(kk[i], mid);
       scan_excl<int64_t>(c, tmp, n);
       if (n <= p.n_wg) {
         piece = (int)mid;
@@ -87,6 +90,19 @@ __device__ void make_plan(const LatentPlan &p, uint8_t *lds) {
         lo = mid + 1;
       }
     }
+    // Whole row tiles where those are no more than a few cache tiles longer: the join of 256 pieces of 128 rows costs 12
+    // to 17 us, a cache tile 1.9 us (128 heads, 128 tokens: the four kernels take 56 us so and 71 us in pieces with
+    // nothing before them, 68 and 78 us with 200 tokens, 78 and 83 us with 400).
+    int most = 1;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (rr[i]) most = max(most, kk[i]);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) most = max(most, __shfl_xor(most, o, 64));
+    if ((tid & 63) == 0) lens[1024 + (tid >> 6)] = most;
+    __syncthreads();
+    for (int w = 0; w < 4; ++w) most = max(most, lens[1024 + w]);
+    if (piece && (most - piece) * 4096 <= p.n_wg * p.rows) piece = max(piece, most);
   }
   // even runs: where a workgroup has few cache tiles it is better off with fewer of them than with even work
   const int over = !piece && total >= 4 * (int64_t)p.n_wg ? p.over : 0;
@@ -100,7 +116,7 @@ __device__ void make_plan(const LatentPlan &p, uint8_t *lds) {
     at0 += (int64_t)rr[i] * (piece ? (kk[i] + piece - 1) / piece : kk[i] + over);
   }
   __syncthreads();
-  const int64_t per = piece ? 1 : max((all + p.n_wg - 1) / p.n_wg, (int64_t)1);
+  const int64_t per = piece ? 1 : max(div_up(all, p.n_wg), (int64_t)1);
   int shared0 = 0;
   for (int w0 = 0; w0 < p.n_wg; w0 += 256) {
     const int w = w0 + tid;
@@ -110,16 +126,17 @@ __device__ void make_plan(const LatentPlan &p, uint8_t *lds) {
     if (w < p.n_wg && v < all) {
       // the last sequence that starts at or before v is the one that has it: those without units share their
       // successor's start
-      const int b = last_at_or_below(start, 1024, v);
+      const int b = last_at_or_below(start, p.a.B, v);
       const int k = tiles_of(lens[b]);
       const uint32_t r = (uint32_t)min(v - start[b], (int64_t)0x7fffffff);
       d = WgDesc{b, 0, 0, 0, t0s[b], nqs[b], lens[b], over};
       if (piece) {
-        const int c = (k + piece - 1) / piece, i = r % (uint32_t)c;  // piece i of c of row tile mt
-        d.mt = r / (uint32_t)c;
-        d.at = (int)((int64_t)k * i / c);
-        d.n = (int)((int64_t)k * (i + 1) / c) - d.at;
-        if (i == 0 && c > 1) t = TileDesc{b, d.mt, w, w + c - 1, 0};
+        // piece i of c of row tile mt; a piece's row tiles are neighbours, which read the same cache rows
+        const int c = (k + piece - 1) / piece, tiles = (nqs[b] * p.a.H + p.rows - 1) / p.rows, i = r / (uint32_t)tiles;
+        d.mt = r % (uint32_t)tiles;
+        d.at = i * (k / c) + min(i, k % c);
+        d.n = k / c + (i < k % c ? 1 : 0);
+        if (i == 0 && c > 1) t = TileDesc{b, d.mt, w, c, tiles, 0};
       } else {
         d.mt = r / (uint32_t)(k + over);
         d.at = r % (uint32_t)(k + over);
@@ -127,91 +144,92 @@ __device__ void make_plan(const LatentPlan &p, uint8_t *lds) {
         // shared with the workgroups before, and the first boundary in this row tile
         const int64_t u0 = v - d.at;
         const int first = (int)((u0 + over) / per);
-        if (d.at > over && first == w - 1) t = TileDesc{b, d.mt, first, (int)((u0 + over + k - 1) / per), u0};
+        if (d.at > over && first == w - 1)
+          t = TileDesc{b, d.mt, first, (int)((u0 + over + k - 1) / per) - first + 1, 1, u0};
       }
     }
     if (w < p.n_wg) p.wg[w] = d;
     int64_t n;
-    const int64_t at = scan_excl<int64_t>(t.w1 > 0, tmp, n);
-    if (t.w1 > 0) p.shared[shared0 + at] = t;
+    const int64_t at = scan_excl<int64_t>(t.n > 0, tmp, n);
+    if (t.n > 0) p.shared[shared0 + at] = t;
     shared0 += (int)n;
   }
   if (tid == 0) *p.head = PlanHead{per, shared0};
 }
 
-// --- many rows: tiles of 128 rows x 64 or 128 columns through LDS --------------
+// --- more rows: tiles of 64 or 128 rows x 64 or 128 columns through LDS --------
 // Steps of 64 k: a row's 128 bytes of a step lie in LDS as 8 units of 16, unit c
-// at c ^ swz(row) (16 rows' equal units then spread over the 64 banks). Two
-// stages: one is read while the other is loaded.
-constexpr int kBM = 128, kBK = 64;
+// at c ^ swz(row) (16 rows' equal units then spread over the 64 banks). One stage
+// is read while the others are loaded; two workgroups a CU, of 128 x 128 with two
+// stages, of the smaller tiles with three (128 heads, 64 tokens: 13.6 and 8.8 us
+// for the absorbed queries and the last product with tiles of 64 x 128, 14.3 and
+// 11.4 us with 128 x 128; 512 tokens: 34.6 and 24.1 us with 128 x 128, 40.3 and
+// 32.2 us with 128 x 64, which are for 64 columns only).
+constexpr int kBK = 64;
 
 __device__ __forceinline__ int swz(int row) { return ((row >> 1 & 1) << 2) | (row >> 2 & 3); }
 
-template <typename E, int BN>
+template <typename E, int BM, int BN>
 __global__ __launch_bounds__(256, 2) void head_gemm_tile_kernel(HeadGemm g, LatentPlan plan) {
-  constexpr int kStage = (kBM + BN) * 128, kNB = BN / 64;  // blocks of 32 n of a wave
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
+  constexpr int kStage = (BM + BN) * 128, kStages = 3 * kStage <= 80 << 10 ? 3 : 2;
+  constexpr int kNB = BN / 64, kMB = BM / 64;        // blocks of 32 columns and of 32 rows of a wave
+  constexpr int kA = BM / 32, kLoads = kA + BN / 32;  // loads of a wave and stage: 8 rows x 128 bytes each
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages * kStage];
   if (plan.n_wg && blockIdx.x == gridDim.x - 1) {
     if (blockIdx.y == 0) make_plan(plan, lds);
     return;
   }
-  const int M = g.hi ? min(g.M, uniform(*g.hi)) : g.M, lo = g.lo ? uniform(*g.lo) : 0;
   const int n_tiles = g.N / BN;
-  const int m0 = blockIdx.x / n_tiles * kBM, n0 = blockIdx.x % n_tiles * BN, h = blockIdx.y;
-  if (m0 >= M || m0 + kBM <= lo) return;
+  const int m0 = blockIdx.x / n_tiles * BM, n0 = blockIdx.x % n_tiles * BN, h = blockIdx.y;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int wm = (wave & 1) * 64, wn = (wave >> 1) * (BN / 2), l32 = lane & 31, hl = lane >> 5;
+  const int wm = (wave & 1) * (BM / 2), wn = (wave >> 1) * (BN / 2), l32 = lane & 31, hl = lane >> 5;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
-  // loads: 8 rows x 128 bytes a wave and instruction; lane's row in the block and its unit
-  const int r8 = lane >> 3;
-  const uint16_t *a_src[kBM / 32];
-  const uint16_t *b_src[BN / 32];
+  const uint16_t *src[kLoads];
 #pragma unroll
-  for (int i = 0; i < kBM / 32; ++i) {
-    const int r = (i * 4 + wave) * 8 + r8, m = min(m0 + r, M - 1);
-    a_src[i] = g.A + (int64_t)m * g.a_m + h * g.a_h + ((lane & 7) ^ swz(r & 15)) * 8;
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = ((i < kA ? i : i - kA) * 4 + wave) * 8 + (lane >> 3);
+    src[i] = (i < kA ? g.A + (int64_t)min(m0 + r, g.M - 1) * g.a_m + h * g.a_h
+                     : g.B + h * g.b_h + (int64_t)(n0 + r) * g.K) +
+             ((lane & 7) ^ swz(r & 15)) * 8;
   }
+  auto load = [&](int s) {  // behind the last step nothing is loaded (but counted)
+    const uint32_t to = uniform(lds0 + s % kStages * kStage + wave * 1024);
+    const int on = uniform(s * kBK < g.K ? -1 : 0);
 #pragma unroll
-  for (int i = 0; i < BN / 32; ++i) {
-    const int r = (i * 4 + wave) * 8 + r8;
-    b_src[i] = g.B + h * g.b_h + (int64_t)(n0 + r) * g.K + ((lane & 7) ^ swz(r & 15)) * 8;
-  }
-  auto load = [&](int stage, int k0) {
-    const uint32_t to = uniform(lds0 + stage * kStage + wave * 1024);
-#pragma unroll
-    for (int i = 0; i < kBM / 32; ++i) lds_load16<0>(a_src[i] + k0, to + i * 4096);
-#pragma unroll
-    for (int i = 0; i < BN / 32; ++i) lds_load16<0>(b_src[i] + k0, to + kBM * 128 + i * 4096);
+    for (int i = 0; i < kLoads; ++i)
+      lds_load16<0>(src[i] + s * kBK, to + (i < kA ? i * 4096 : BM * 128 + (i - kA) * 4096), on);
   };
-  f32x16 acc[kNB][2];
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) load(s);
+  f32x16 acc[kNB][kMB];
 #pragma unroll
   for (int i = 0; i < kNB; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+    for (int j = 0; j < kMB; ++j) acc[i][j] = f32x16{};
   int off[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) off[k] = l32 * 128 + (((2 * k + hl) ^ swz(l32 & 15)) << 4);
-  load(0, 0);
-  for (int k0 = 0, st = 0; k0 < g.K; k0 += kBK, st ^= 1) {
-    WAIT_VM(0);
+  for (int s = 0; s * kBK < g.K; ++s) {
+    WAIT_VM((kStages - 2) * kLoads);
     asm volatile("s_barrier" ::: "memory");
-    if (k0 + kBK < g.K) load(st ^ 1, k0 + kBK);
-    const uint8_t *as = lds + st * kStage + wm * 128, *bs = lds + st * kStage + (kBM + wn) * 128;
+    load(s + kStages - 1);
+    const uint8_t *as = lds + s % kStages * kStage + wm * 128, *bs = lds + s % kStages * kStage + (BM + wn) * 128;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      u16x8 af[2], bf[kNB];
+      u16x8 af[kMB], bf[kNB];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) af[j] = *reinterpret_cast<const u16x8 *>(as + j * 4096 + off[k]);
+      for (int j = 0; j < kMB; ++j) af[j] = *reinterpret_cast<const u16x8 *>(as + j * 4096 + off[k]);
 #pragma unroll
       for (int i = 0; i < kNB; ++i) bf[i] = *reinterpret_cast<const u16x8 *>(bs + i * 4096 + off[k]);
 #pragma unroll
       for (int i = 0; i < kNB; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = E::mfma(bf[i], af[j], acc[i][j]);
+        for (int j = 0; j < kMB; ++j) acc[i][j] = E::mfma(bf[i], af[j], acc[i][j]);
     }
   }
+  const int M = g.hi ? min(g.M, *g.hi) : g.M, lo = g.lo ? *g.lo : 0;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < kMB; ++j) {
     const int m = m0 + wm + 32 * j + l32;
     uint16_t *c = g.C + m * g.c_m + h * g.c_h + n0 + wn + 8 * hl;
 #pragma unroll
@@ -230,8 +248,10 @@ __global__ __launch_bounds__(256, 2) void head_gemm_tile_kernel(HeadGemm g, Late
 // A workgroup takes 32 rows x 32 columns, each wave a quarter of k: both operands
 // come from memory straight in the products' layout (16 bytes a lane, a column's
 // k in order), all of a wave's loads in flight at once; the quarters are summed
-// through LDS.
-constexpr int kPlanLds = 8 * 1024 + 64 + 3 * 4096;
+// through LDS. 128 heads, 8 tokens (17 MB of weights each): 7.0 and 5.6 us. Twice
+// and four times the rows so were no faster than tiles: 16.0 and 16.7 us for 64
+// tokens, against 13.6 and 8.8.
+constexpr int kPlanLds = 8 * 1024 + 64 + 3 * 4096 + 16;
 
 template <typename E>
 __global__ __launch_bounds__(256) void head_gemm_stream_kernel(HeadGemm g, LatentPlan plan) {
@@ -395,11 +415,13 @@ void launch(moe_ctx *ctx, const HeadGemm &g, int H, const LatentPlan &p) {
   if (g.M <= 32)
     hipLaunchKernelGGL(head_gemm_stream_kernel<E>, dim3(g.N / 32 + extra, H, (g.M + 31) / 32), dim3(256), 0,
                        ctx->stream, g, p);
+  else if (g.M <= 64 && g.N % 128 == 0)
+    hipLaunchKernelGGL((head_gemm_tile_kernel<E, 64, 128>), dim3(g.N / 128 + extra, H), dim3(256), 0, ctx->stream, g, p);
   else if (g.N % 128 == 0)
-    hipLaunchKernelGGL((head_gemm_tile_kernel<E, 128>), dim3((g.M + kBM - 1) / kBM * (g.N / 128) + extra, H), dim3(256),
+    hipLaunchKernelGGL((head_gemm_tile_kernel<E, 128, 128>), dim3((g.M + 127) / 128 * (g.N / 128) + extra, H), dim3(256),
                        0, ctx->stream, g, p);
   else
-    hipLaunchKernelGGL((head_gemm_tile_kernel<E, 64>), dim3((g.M + kBM - 1) / kBM * (g.N / 64) + extra, H), dim3(256),
+    hipLaunchKernelGGL((head_gemm_tile_kernel<E, 128, 64>), dim3((g.M + 127) / 128 * (g.N / 64) + extra, H), dim3(256),
                        0, ctx->stream, g, p);
 }
 

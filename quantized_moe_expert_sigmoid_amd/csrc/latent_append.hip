@@ -1,6 +1,9 @@
 // Writer of the latent cache: norm of the latents, rotation of the keys' and
 // the queries' rotary parts. One pass over the data; a wave takes one token's
-// row (a 16-byte unit a lane) or 64 units of the queries' rotary parts.
+// row (a 16-byte unit a lane) or 64 units of the queries' rotary parts. Sums and
+// rotations are fp32, rounded once to the element type. The bytes are the bound:
+// 5800 tokens of 64 heads read and write 106 MB in 23 us, 4.6 TB/s (a large copy:
+// 4.9); one token is a launch of 2.8 us.
 #include "latent.h"
 
 namespace {

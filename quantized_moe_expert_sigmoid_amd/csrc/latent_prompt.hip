@@ -7,12 +7,21 @@
 // that one wave's exponentials run under the other's products; its tiles of keys and
 // values come into LDS by asynchronous loads, one being read, the others in
 // flight.
+//
+// Statistics, scores and sums are fp32; the expanded keys and values and P^T are
+// rounded to the element type, since the products read elements and 32 bits would
+// double the workspace's bytes (0.0028 relative in bf16, 0.0017 of it the output's
+// own rounding).
+//
+// Measured (128 heads, keys of 128 + 64, values of 128, 4096 tokens): rows 7 us,
+// expansion 163 us (latent_gemm.hip), attention 745 us, 687 GFLOP at 920 TFLOP/s,
+// where the library's product of 8192 x 8192 x 8192 reaches 1350. The products
+// bound it, at the clock (1.7 to 2.1 GHz) that they leave.
 #include "latent.h"
 
 #include <algorithm>
 
 namespace {
-
 
 // The plan: off[b] = first expanded row of sequence b (B + 1 entries), the
 // row tiles. Sequences that do not fit n_kv rows are

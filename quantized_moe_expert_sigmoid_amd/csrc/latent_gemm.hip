@@ -102,7 +102,7 @@ __device__ void make_plan(const LatentPlan &p, uint8_t *lds) {
     if ((tid & 63) == 0) lens[1024 + (tid >> 6)] = most;
     __syncthreads();
     for (int w = 0; w < 4; ++w) most = max(most, lens[1024 + w]);
-    if (piece && (most - piece) * 4096 <= p.n_wg * p.rows) piece = max(piece, most);
+    if (piece && most - piece <= p.n_wg * p.rows / 4096) piece = max(piece, most);
   }
   // even runs: where a workgroup has few cache tiles it is better off with fewer of them than with even work
   const int over = !piece && total >= 4 * (int64_t)p.n_wg ? p.over : 0;

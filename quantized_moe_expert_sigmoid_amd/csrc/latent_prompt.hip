@@ -38,6 +38,7 @@ struct PromptWs {
   uint16_t *x;       // [H][n_kv][dn + dv] keys and values
   int64_t n_kv;
   int tile_rows;     // query tokens of a row tile
+  int max_tiles;     // row tiles of T tokens at most; starts that go back (reported) could ask for more
 };
 
 // The sequences' cache rows one after another (a wave a row, 16 bytes a lane, the
@@ -81,6 +82,7 @@ __global__ __launch_bounds__(256) void prompt_rows_kernel(LatentArgs a, PromptWs
     tbefore += w < wave ? tmp[4 + w] : 0;
     n_tiles += tmp[4 + w];
   }
+  const bool sorted = n_tiles <= min(kSort, ws.max_tiles);
   int64_t o = before + at - sum;
   int t = tbefore + tat - tsum;
 #pragma unroll
@@ -91,8 +93,8 @@ __global__ __launch_bounds__(256) void prompt_rows_kernel(LatentArgs a, PromptWs
     if (first && b < a.B) {
       if (!fits) atomicOr(a.err, (uint32_t)ERRF_LATENT);
       ws.off[b] = fits ? (int)o : -1;
-      if (n_tiles > kSort)
-        for (int k = 0; k < nt[i]; ++k) ws.tile[t + k] = PromptTile{b, k * ws.tile_rows};
+      if (!sorted)
+        for (int k = 0; k < nt[i] && t + k < ws.max_tiles; ++k) ws.tile[t + k] = PromptTile{b, k * ws.tile_rows};
       else
         for (int k = 0; k < nt[i]; ++k) {
           tile_s[t + k] = PromptTile{b, k * ws.tile_rows};
@@ -105,9 +107,9 @@ __global__ __launch_bounds__(256) void prompt_rows_kernel(LatentArgs a, PromptWs
     o += len[i];
     t += nt[i];
   }
-  if (first && tid == 0) *ws.n_tiles = n_tiles;
+  if (first && tid == 0) *ws.n_tiles = min(n_tiles, ws.max_tiles);
   __syncthreads();
-  if (first && n_tiles <= kSort && tid < n_tiles) {
+  if (first && sorted && tid < n_tiles) {
     const int mine = sees[tid];
     int rank = 0;
     for (int x = 0; x < n_tiles; ++x) rank += sees[x] > mine || (sees[x] == mine && x < tid);
@@ -395,7 +397,8 @@ moe_status launch(moe_ctx *ctx, const LatentArgs &a, int64_t n_kv) {
                     reinterpret_cast<PromptTile *>(p + o_tile), reinterpret_cast<uint16_t *>(p + o_c),
                     reinterpret_cast<uint16_t *>(p + o_kr),  reinterpret_cast<uint16_t *>(p + o_x),
                     n_kv,
-                    kRows};
+                    kRows,
+                    (int)tiles};
   const unsigned row_blocks = (unsigned)std::max<int64_t>(1, std::min<int64_t>((n_kv + 3) / 4, 1024));
   hipLaunchKernelGGL(prompt_rows_kernel, dim3(row_blocks), dim3(256), 0, ctx->stream, a, ws);
   MOE_CHECK_LAUNCH("prompt_rows_kernel");

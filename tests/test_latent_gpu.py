@@ -512,6 +512,20 @@ def test_bad_bounds_are_reported(moe, ctx, form, what):
     ctx.check()  # cleared
 
 
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
+@pytest.mark.parametrize("back", [0, 90])
+def test_starts_that_go_back_are_reported(moe, ctx, form, back):
+    """Sequences that share queries ask for more row tiles than T tokens have."""
+    p = Problem(74, [130] + [0] * 7, [150] + [20] * 7, **TINY)
+    d = p.gpu()
+    d["kv_len"].fill_(20)
+    d["q_start"][2:] = torch.tensor([back, 130, back, 130, back, 130, 130], dtype=torch.int32)
+    p.run(moe, ctx, form, d, n_kv=200)
+    with pytest.raises(moe.MoeError):
+        ctx.check()
+    p.check(moe, ctx, form)
+
+
 def test_too_small_a_workspace_is_reported(moe, ctx):
     p = Problem(72, [1, 2, 1], [40, 20, 30], **TINY)
     ref, tol = p.reference("expanded")

@@ -7,6 +7,8 @@ sequences' pages and lengths are kept on the host and sent with each call.
 """
 from __future__ import annotations
 
+import itertools
+
 import torch
 
 from . import LatentCfg, MoeCtx, moe_latent_append, moe_latent_attend, moe_latent_prompt
@@ -23,10 +25,12 @@ class LatentAttention:
                  device: str = "cuda"):
         self.ctx, self.eps, self.device = ctx, eps, device
         self.cfg = LatentCfg(n_heads, d_latent, d_rope, d_nope, d_v, dtype, page_size)
-        self.cache = torch.zeros((n_pages, page_size, d_latent + d_rope), dtype=dtype, device=device)
+        with torch.cuda.stream(ctx.stream):
+            self.cache = torch.zeros((n_pages, page_size, d_latent + d_rope), dtype=dtype, device=device)
         angle = torch.arange(max_positions, dtype=torch.float64)[:, None] * rope_base ** (
             -torch.arange(d_rope // 2, dtype=torch.float64) * 2 / d_rope)
-        self.turn = torch.stack([angle.cos(), angle.sin()], dim=-1).float().to(device)
+        with torch.cuda.stream(ctx.stream):
+            self.turn = torch.stack([angle.cos(), angle.sin()], dim=-1).float().to(device)
         self.w_kv = self.w_kt = self.norm_w = None
         self._free = list(range(n_pages - 1, -1, -1))
         self._pages: dict[int, list[int]] = {}
@@ -37,10 +41,16 @@ class LatentAttention:
     def set_weights(self, w_kv, norm_w=None):
         """w_kv [H][d_nope + d_v][d_latent] (a head's key rows, then its value
         rows), norm_w [d_latent] or None (latents enter the cache as they are)."""
-        c = self.cfg
-        self.w_kv = torch.as_tensor(w_kv).to(device=self.device, dtype=c.dtype).contiguous()
-        self.w_kt = self.w_kv[:, :c.d_nope].transpose(1, 2).contiguous()  # the absorbed form's layout of the key rows
-        self.norm_w = None if norm_w is None else torch.as_tensor(norm_w).to(device=self.device, dtype=torch.float32)
+        c, stream, caller = self.cfg, self.ctx.stream, torch.cuda.current_stream(self.cache.device)
+        stream.wait_stream(caller)  # the weights may still be on their way there
+        with torch.cuda.stream(stream):
+            self.w_kv = torch.as_tensor(w_kv).to(device=self.device, dtype=c.dtype).contiguous()
+            # the absorbed form's layout of the key rows
+            self.w_kt = self.w_kv[:, :c.d_nope].transpose(1, 2).contiguous()
+            self.norm_w = None
+            if norm_w is not None:
+                self.norm_w = torch.as_tensor(norm_w).to(device=self.device, dtype=torch.float32)
+        caller.wait_stream(stream)  # and may be overwritten or freed after the call
 
     # -- sequences ----------------------------------------------------------
     def new_sequence(self) -> int:
@@ -60,11 +70,14 @@ class LatentAttention:
         p = self.cfg.page_size
         return self._pages[seq][j // p] * p + j % p
 
+    def _room(self, need: int):
+        if need > len(self._free):
+            raise RuntimeError(f"latent cache: {need} pages are needed, {len(self._free)} are free")
+
     def _resize(self, seq: int, n: int):
         pages, p = self._pages[seq], self.cfg.page_size
         need = -(-n // p)
-        if need - len(pages) > len(self._free):
-            raise RuntimeError(f"latent cache: sequence {seq} needs {need - len(pages)} pages, {len(self._free)} are free")
+        self._room(need - len(pages))
         while len(pages) < need:
             pages.append(self._free.pop())
         while len(pages) > need:
@@ -80,9 +93,9 @@ class LatentAttention:
             raise ValueError(f"nodes must ascend within 0..{n_own - 1}")
         flat = self.cache.view(-1, self.cache.shape[-1])
         if nodes:
-            src = torch.tensor([self._row(seq, before + v) for v in nodes], device=self.device)
-            dst = torch.tensor([self._row(seq, before + i) for i in range(len(nodes))], device=self.device)
             with torch.cuda.stream(self.ctx.stream):
+                src = torch.tensor([self._row(seq, before + v) for v in nodes], device=self.device)
+                dst = torch.tensor([self._row(seq, before + i) for i in range(len(nodes))], device=self.device)
                 flat[dst] = flat[src]
         self._resize(seq, before + len(nodes))
 
@@ -93,14 +106,27 @@ class LatentAttention:
         projections before norm and rotation, sequence after sequence. tree: the
         tokens' visibility words (ints, bit j: own token j of the sequence) for
         drafts that branch, with depth: each token's distance in positions from
-        its sequence's first new one. Returns [T][H][d_v]."""
+        its sequence's first new one. Returns [T][H][d_v]. What is refused here
+        leaves the sequences as they were."""
         c = self.cfg
         T = sum(counts)
-        if q.shape[0] != T or kv.shape[0] != T or len(seqs) != len(counts) or len(set(seqs)) != len(seqs):
+        if (q.shape[0] != T or kv.shape[0] != T or len(seqs) != len(counts) or len(set(seqs)) != len(seqs) or
+                any(n < 0 for n in counts)):
             raise ValueError("one q and kv row a token, each sequence once")
         if (tree is None) != (depth is None):
             raise ValueError("tree and depth go together")
+        if tree is not None and (len(tree) != T or len(depth) != T or max(counts, default=0) > 64 or
+                                 any(int(d) < 0 for d in depth)):
+            raise ValueError("a word and a depth (from 0) a token, 64 tokens a sequence at most")
+        if self.w_kv is None:
+            raise RuntimeError("set_weights comes first")
         before = [self._len[s] for s in seqs]
+        p = self.cfg.page_size
+        self._room(sum(max(-(-(b + n) // p) - len(self._pages[s]), 0) for s, n, b in zip(seqs, counts, before)))
+        ends = [b + (n if depth is None else 1 + max(map(int, depth[t:t + n]), default=-1))
+                for n, b, t in zip(counts, before, itertools.accumulate(counts, initial=0))]
+        if max(ends, default=0) > self.turn.shape[0]:
+            raise ValueError(f"position {max(ends) - 1} is behind max_positions {self.turn.shape[0]}")
         start, pos, slot = [0], [], []
         for s, n, b in zip(seqs, counts, before):
             self._resize(s, b + n)

@@ -131,6 +131,55 @@ def test_refusals(layer):
     layer.drop_sequence(s)
 
 
+def test_refused_calls_leave_the_sequences_as_they_were(layer):
+    a, b = layer.new_sequence(), layer.new_sequence()
+    q, kv = tokens(31, 700)
+    layer.forward([a], [20], q[:20], kv[:20])
+    free = len(layer._free)
+
+    def refused(error, *args, **kw):
+        with pytest.raises(error):
+            layer.forward(*args, **kw)
+        assert (layer.length(a), layer.length(b), len(layer._free)) == (20, 0, free)
+
+    refused(RuntimeError, [a, b], [20, 680], q, kv)  # room for the first, not for both
+    refused(ValueError, [a, b], [3, 401], q[:404], kv[:404])  # a position behind the table's
+    refused(ValueError, [a], [2], q[:2], kv[:2], tree=[1, 3], depth=[0, 380])
+    refused(ValueError, [a], [2], q[:2], kv[:2], tree=[1, 3], depth=[-1, 0])
+    refused(ValueError, [a], [2], q[:2], kv[:2], tree=[1], depth=[0])
+    refused(ValueError, [a], [65], q[:65], kv[:65], tree=[1] * 65, depth=[0] * 65)
+    refused(ValueError, [a, b], [3, -1], q[:2], kv[:2])
+    layer.drop_sequence(a)
+    layer.drop_sequence(b)
+
+
+def test_layer_on_a_stream_of_its_own(layer):
+    """The same bits as on the default stream, weights and drafts included."""
+    import quantized_moe_expert_sigmoid_amd as moe
+    from quantized_moe_expert_sigmoid_amd.latent import LatentAttention
+    q, kv = tokens(32, 30)
+
+    def steps(L):
+        s = L.new_sequence()
+        outs = [L.forward([s], [20], q[:20], kv[:20]),
+                L.forward([s], [4], q[20:24], kv[20:24], tree=[1, 3, 5, 13], depth=[0, 1, 1, 2])]
+        L.keep(s, 4, [0, 2, 3])
+        outs.append(L.forward([s], [6], q[24:], kv[24:]))
+        L.ctx.check()
+        L.drop_sequence(s)
+        return outs
+
+    want = steps(layer)
+    torch.cuda.synchronize()
+    ctx = moe.MoeCtx(0, torch.cuda.Stream())
+    L = LatentAttention(ctx, H, DC, DR, DN, DV, n_pages=40, page_size=16, max_positions=400, dtype=torch.float16)
+    L.set_weights(layer.w_kv * 1, layer.norm_w * 1)
+    got = steps(L)
+    ctx.stream.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    ctx.close()
+
+
 def test_decoder_layer_example():
     """Prompt, single tokens and a verified draft give what one pass over all tokens gives, up to the roundings of the
     two forms (bf16, u = 2^-8: 4 u of the attention's share of each output is accepted) and the experts' int8

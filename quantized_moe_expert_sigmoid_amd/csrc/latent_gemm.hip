@@ -47,7 +47,10 @@ __device__ void make_plan(const LatentPlan &p, uint8_t *lds) {
   int *t0s = reinterpret_cast<int *>(tmp + 8), *nqs = t0s + 1024, *lens = nqs + 1024;
   const int tid = threadIdx.x;
   auto tiles_of = [&](int len) { return max(1, (len + p.tokens - 1) / p.tokens); };
-  int64_t u = 0, rt = 0;
+  const int row_shift = __ffs(p.rows) - 1;
+  auto rows_of = [&](int nq) { return (nq * p.a.H + p.rows - 1) >> row_shift; };
+  int64_t u = 0;
+  int rt = 0, most = 1;  // row tiles (above the workgroups' number only that they are matters), the longest one's cache tiles
   int rr[kPer], kk[kPer];  // row tiles, cache tiles
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -59,50 +62,64 @@ __device__ void make_plan(const LatentPlan &p, uint8_t *lds) {
       t0s[b] = s.t0;
       nqs[b] = s.nq;
       lens[b] = s.len;
-      rr[i] = (s.nq * p.a.H + p.rows - 1) / p.rows;
+      rr[i] = rows_of(s.nq);
       kk[i] = tiles_of(s.len);
+      if (rr[i]) most = max(most, kk[i]);
     }
     u += (int64_t)rr[i] * kk[i];
-    rt += rr[i];
+    rt += min(rr[i], 1 << 20);
   }
-  int64_t total, n_rows;
-  scan_excl<int64_t>(u, tmp, total);
-  scan_excl<int64_t>(rt, tmp, n_rows);
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    u += __shfl_xor(u, o, 64);
+    rt += __shfl_xor(rt, o, 64);
+    most = max(most, __shfl_xor(most, o, 64));
+  }
+  int *tmp32 = reinterpret_cast<int *>(tmp + 4);
+  if ((tid & 63) == 0) {
+    tmp[tid >> 6] = u;
+    tmp32[tid >> 6] = rt;
+    tmp32[4 + (tid >> 6)] = most;
+  }
+  __syncthreads();
+  int64_t total = 0;
+  int n_rows = 0;
+  for (int w = 0; w < 4; ++w) {
+    total += tmp[w];
+    n_rows += tmp32[w];
+    most = max(most, tmp32[4 + w]);
+  }
+  __syncthreads();
   auto div_up = [](int64_t x, int64_t y) {  // 64-bit division is slow, and rarely needed
     return x + y < (1ll << 31) ? (int64_t)(((uint32_t)x + (uint32_t)y - 1) / (uint32_t)y) : (x + y - 1) / y;
   };
   const int64_t even = div_up(total, p.n_wg);
 
-  // the smallest pieces that are no more than the workgroups
+  // the smallest pieces that are no more than the workgroups: 16 sizes at a time, 16 threads a size
   int piece = 0;
   if (n_rows > 0 && n_rows < p.n_wg) {
-    int64_t lo = even, hi = min(even + p.over, div_up(total, p.n_wg - n_rows));
-    while (lo <= hi) {
-      const int64_t mid = (lo + hi) >> 1;
-      int64_t c = 0, n;
+    const int64_t size = even + (tid >> 4), top = min(even + min(p.over, 15), div_up(total, p.n_wg - n_rows));
+    int c = 0;
+    if (size <= top)
+      for (int b = tid & 15; b < p.a.B; b += 16)
+        c += (int)min((int64_t)rows_of(nqs[b]) * (int64_t)(((uint32_t)tiles_of(lens[b]) + (uint32_t)size - 1) / (uint32_t)size),
+                      (int64_t)1 << 20);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) c += (int64_t)rr[i] * div_up(kk[i], mid);
-      scan_excl<int64_t>(c, tmp, n);
-      if (n <= p.n_wg) {
-        piece = (int)mid;
-        hi = mid - 1;
-      } else {
-        lo = mid + 1;
-      }
-    }
-    // Whole row tiles where those are no more than a few cache tiles longer: the join of 256 pieces of 128 rows costs 12
-    // to 17 us, a cache tile 1.9 us (128 heads, 128 tokens: the four kernels take 56 us so and 71 us in pieces with
-    // nothing before them, 68 and 78 us with 200 tokens, 78 and 83 us with 400).
-    int most = 1;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (rr[i]) most = max(most, kk[i]);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) most = max(most, __shfl_xor(most, o, 64));
-    if ((tid & 63) == 0) lens[1024 + (tid >> 6)] = most;
+    for (int o = 1; o < 16; o <<= 1) c += __shfl_xor(c, o, 64);
+    const uint64_t fit = __ballot(size <= top && c <= p.n_wg);
+    const int lane = fit ? __ffsll((unsigned long long)fit) - 1 : 0, pieces = __shfl(c, lane, 64);
+    if ((tid & 63) == 0) tmp32[tid >> 6] = fit ? ((tid >> 6) * 4 + lane / 16) << 16 | pieces : 16 << 16;
     __syncthreads();
-    for (int w = 0; w < 4; ++w) most = max(most, lens[1024 + w]);
-    if (piece && most - piece <= p.n_wg * p.rows / 4096) piece = max(piece, most);
+    const int best = min(min(tmp32[0], tmp32[1]), min(tmp32[2], tmp32[3]));
+    __syncthreads();
+    if (best < 16 << 16) {
+      piece = (int)even + (best >> 16);
+      // Whole row tiles where those are no more than a few cache tiles longer: the join of 256 pieces of 128 rows costs
+      // 12 to 17 us, a cache tile 1.9 us (128 heads, 128 tokens of one sequence: the four kernels take 56 us so and 71
+      // us in pieces with nothing before them, 68 and 78 us with 200 tokens, 78 and 83 us with 400; but one token over
+      // 101 rows, whose pieces are 4, 35 us and 31 us).
+      if (most - piece <= (best & 0xffff) * p.rows / 4096) piece = max(piece, most);
+    }
   }
   // even runs: where a workgroup has few cache tiles it is better off with fewer of them than with even work
   const int over = !piece && total >= 4 * (int64_t)p.n_wg ? p.over : 0;
@@ -132,7 +149,7 @@ __device__ void make_plan(const LatentPlan &p, uint8_t *lds) {
       d = WgDesc{b, 0, 0, 0, t0s[b], nqs[b], lens[b], over};
       if (piece) {
         // piece i of c of row tile mt; a piece's row tiles are neighbours, which read the same cache rows
-        const int c = (k + piece - 1) / piece, tiles = (nqs[b] * p.a.H + p.rows - 1) / p.rows, i = r / (uint32_t)tiles;
+        const int c = (k + piece - 1) / piece, tiles = rows_of(nqs[b]), i = r / (uint32_t)tiles;
         d.mt = r % (uint32_t)tiles;
         d.at = i * (k / c) + min(i, k % c);
         d.n = k / c + (i < k % c ? 1 : 0);
@@ -149,10 +166,10 @@ __device__ void make_plan(const LatentPlan &p, uint8_t *lds) {
       }
     }
     if (w < p.n_wg) p.wg[w] = d;
-    int64_t n;
-    const int64_t at = scan_excl<int64_t>(t.n > 0, tmp, n);
+    int n;
+    const int at = scan_excl<int>(t.n > 0, tmp32, n);
     if (t.n > 0) p.shared[shared0 + at] = t;
-    shared0 += (int)n;
+    shared0 += n;
   }
   if (tid == 0) *p.head = PlanHead{per, shared0};
 }
@@ -251,7 +268,7 @@ __global__ __launch_bounds__(256, 2) void head_gemm_tile_kernel(HeadGemm g, Late
 // through LDS. 128 heads, 8 tokens (17 MB of weights each): 7.0 and 5.6 us. Twice
 // and four times the rows so were no faster than tiles: 16.0 and 16.7 us for 64
 // tokens, against 13.6 and 8.8.
-constexpr int kPlanLds = 8 * 1024 + 64 + 3 * 4096 + 16;
+constexpr int kPlanLds = 8 * 1024 + 64 + 3 * 4096;
 
 template <typename E>
 __global__ __launch_bounds__(256) void head_gemm_stream_kernel(HeadGemm g, LatentPlan plan) {

@@ -490,7 +490,8 @@ int moe_pool_resident(const moe_pool *pool, int layer, int expert);
  * Elements (queries, cache, weights, out) are bf16 or fp16; scores, softmax
  * statistics and every sum are fp32. Rounded to the element type on the way:
  * a, the softmax weights before they multiply values, sum_j p_j c_j (both
- * forms' last product takes elements), and the expanded keys and values.
+ * forms' last product takes elements), and the expanded keys and values (one
+ * beyond the type's range is infinite for the queries that see its row).
  *
  * The cache is pages of page_size rows: [n_pages][page_size][d_latent +
  * d_rope]. Sequence b has kv_len[b] cached rows, the call's own tokens last;

@@ -236,6 +236,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void latent_prompt_kernel(LatentArgs
 #pragma unroll
   for (int i = 0; i < kNB; ++i) acc[i] = f32x16{};
   float m = -__builtin_inff(), l = 0.0f;
+  int cleared = s.len;  // first position of a tile whose values were partly cleared
   if (n > 0)
 #pragma unroll
     for (int i = 0; i < C::kBufs - 1; ++i) {
@@ -290,43 +291,54 @@ __global__ __launch_bounds__(64 * W, W / 4) void latent_prompt_kernel(LatentArgs
         const int c = min(max(min(s.before + qi + 1, s.len) - j0, 0), 64);
         return c == 64 ? ~0ull : (1ull << c) - 1;
       }() >> (4 * hl);
-      bool odd = false;
+      // A value that is NaN or infinite would reach the rows that do not see it as 0 x NaN or 0 x inf. Its score does not
+      // tell: keys and values are products of their own, and a value may leave the elements' range where the score stays
+      // finite. So the values themselves are looked at, 8 to 32 of them a lane; in the rare tile that has such elements
+      // they are cleared here, and added at the end for the rows that see them.
+      const int row = lane & (kNT - 1);
+      auto unit = [&](int c) {
+        return reinterpret_cast<u32x4 *>(vv + (c >> 3) * C::kPanelB + row * 128 + (((c & 7) ^ swz(row & 15)) << 4));
+      };
+      // the sign bits of elements whose exponent bits are all set: one more at their low end carries into it
+      auto flags = [](uint32_t x) { return ((x & E::kExp * 0x10001u) + (E::kExp & -E::kExp) * 0x10001u) & 0x80008000u; };
+      auto any_flag = [&](u32x4 x) { return (flags(x[0]) | flags(x[1]) | flags(x[2]) | flags(x[3])) != 0; };
+      constexpr int kShare = W * 64 / kNT;  // units looked at at a time
+      static_assert(DV / 8 % kShare == 0, "");
+      const int c0 = wave * (64 / kNT) + lane / kNT;
+      bool broken = false;
 #pragma unroll
-      for (int tb = 0; tb < kTB; ++tb)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const bool v = (vis64 >> (32 * tb + 8 * (i >> 2) + (i & 3))) & 1;
-          odd |= !v & !(__builtin_fabsf(z[tb][i]) < __builtin_inff());
-          z[tb][i] = v ? z[tb][i] : -__builtin_inff();
-        }
-      // An unseen row that holds NaN or infinities would reach the sums as 0 x NaN: see latent_attend.hip.
-      if (__syncthreads_or(odd)) {
-        bool broken = false;
-        const int row = lane & (kNT - 1);
+      for (int c = 0; c < DV / 8; c += kShare) broken |= any_flag(*unit(c + c0));
+      if (__syncthreads_or(broken)) {
+        cleared = min(cleared, j0);
+        broken = false;
 #pragma unroll 1
-        for (int c = 0; c < DV / 8; ++c) {
-          const u16x8 v = *reinterpret_cast<const u16x8 *>(vv + (c >> 3) * C::kPanelB + row * 128 +
-                                                           (((c & 7) ^ swz(row & 15)) << 4));
-#pragma unroll
-          for (int e = 0; e < 8; ++e) broken |= (v[e] & E::kExp) == E::kExp;
-        }
-        const uint64_t bad = __ballot(broken);
+        for (int c = 0; c < DV / 8; ++c) broken |= any_flag(*unit(c));
+        const uint64_t bad = __ballot(broken);  // of 32 tokens: twice
         __syncthreads();
-        if (broken)
 #pragma unroll 1
-          for (int c = wave; c < DV / 8; c += W)
-            *reinterpret_cast<u32x4 *>(vv + (c >> 3) * C::kPanelB + row * 128 + (((c & 7) ^ swz(row & 15)) << 4)) =
-                u32x4{0, 0, 0, 0};
+        for (int c = c0; c < DV / 8; c += kShare) {
+          u32x4 x = *unit(c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] &= ~((flags(x[e]) >> 15) * 0xffffu);
+          *unit(c) = x;
+        }
+        // a row that sees one behind a score of -inf: 0 x inf
 #pragma unroll
         for (int tb = 0; tb < kTB; ++tb)
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            z[tb][i] = (bad >> (32 * tb + 8 * (i >> 2) + 4 * hl + (i & 3))) & 1 ? -__builtin_inff() : z[tb][i];
-        if (bad & (kNT == 64 ? ~0ull : 0xffffffffull) & (vis64 << (4 * hl))) l = __builtin_nanf("");
+          for (int i = 0; i < 16; ++i) {
+            const int j = 32 * tb + 8 * (i >> 2) + (i & 3);
+            l = ((vis64 & (bad >> (4 * hl))) >> j & 1) & (z[tb][i] == -__builtin_inff()) ? __builtin_nanf("") : l;
+          }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kAhead && i < kV; ++i) ring[(kZ + i) % kAhead] = v_read(i);  // once more
       }
+#pragma unroll
+      for (int tb = 0; tb < kTB; ++tb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          z[tb][i] = (vis64 >> (32 * tb + 8 * (i >> 2) + (i & 3))) & 1 ? z[tb][i] : -__builtin_inff();
     }
     if (j0 >= w_end) continue;  // nothing of this tile is seen by the wave
     float top = z[0][0];
@@ -371,14 +383,27 @@ __global__ __launch_bounds__(64 * W, W / 4) void latent_prompt_kernel(LatentArgs
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint16_t *o = static_cast<uint16_t *>(a.out) + ((int64_t)t * a.H + h) * DV + 8 * hl;
 #pragma unroll
-  for (int i = 0; i < kNB; ++i)
+  for (int i = 0; i < kNB; ++i) {
+    f32x16 r = acc[i] * inv;
+    // what was cleared, for the rows that see it: any weight times NaN or an infinity is that again
+#pragma unroll 1
+    for (int j = cleared; j < w_end; ++j) {
+      const uint8_t *v = xh + (int64_t)j * (DX * 2) + (DN + 32 * i) * 2 + 8 * hl;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const u16x4 x = *reinterpret_cast<const u16x4 *>(v + 16 * g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          r[4 * g + e] += (j <= s.before + qi) & ((x[e] & E::kExp) == E::kExp) ? E::to_f32(x[e]) : 0.0f;
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {
-      const f32x16 r = acc[i] * inv;
       const u32x4 v = rows8<E>(f32x4{r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]},
                                f32x4{r[4 * j + 4], r[4 * j + 5], r[4 * j + 6], r[4 * j + 7]});
       if (live) *reinterpret_cast<u32x4 *>(o + 32 * i + 8 * j) = v;
     }
+  }
 }
 
 template <typename E, int DN, int DR, int DV, int W>

@@ -562,7 +562,9 @@ moe_status moe_latent_append(moe_ctx *ctx, const moe_latent_cfg *cfg, int T, con
  * zeros. What a query does not see has no part in its result, whatever it
  * holds (NaN and infinities included).
  * Nothing about the lengths is read on the host: a captured graph may be
- * replayed on other lengths, tables and masks. */
+ * replayed on other lengths, tables and masks. Calls of more than about 2^39
+ * pairs of 32 cached rows and 32 to 128 query rows (hours of work) are reported
+ * by moe_ctx_check and not computed. */
 moe_status moe_latent_attend(moe_ctx *ctx, const moe_latent_cfg *cfg, const moe_latent_call *call, const void *w_kt,
                              const void *w_kv, const uint64_t *tree, int max_q);
 

@@ -3,6 +3,7 @@
 
 #include <type_traits>
 
+#include "latent_plan.h"
 #include "moe_internal.h"
 
 // One call's arrays as the kernels see them (device pointers, strides in elements).
@@ -42,17 +43,8 @@ moe_status launch_latent_append(moe_ctx *ctx, int dtype, const LatentAppendArgs 
 moe_status launch_latent_attend(moe_ctx *ctx, int dtype, const LatentArgs &a, int max_q);
 moe_status launch_latent_prompt(moe_ctx *ctx, int dtype, const LatentArgs &a, int64_t n_kv);
 
-// How the absorbed form's work is shared out (see latent_attend.hip), written
-// by one workgroup of the kernel that absorbs the queries.
-struct alignas(32) WgDesc {
-  int b, mt, at, n;       // first unit: sequence, row tile, place in the row tile's units; number of units
-  int t0, nq, len, over;  // the sequence's bounds; units a row tile has ahead of its cache tiles
-};
-struct TileDesc {
-  int b, mt, w0, n;  // a row tile whose cache tiles n workgroups share: w0, w0 + step, ..
-  int step;
-  int64_t u0;        // its first unit
-};
+// How the absorbed form's work is shared out (latent_plan.h), written by one
+// workgroup of the kernel that absorbs the queries.
 struct PlanHead {
   int64_t per;   // units of a workgroup
   int n_shared;  // TileDescs

@@ -29,15 +29,6 @@ __device__ T scan_excl(T v, T *tmp, T &total) {  // exclusive sums over the work
   return before + s - v;
 }
 
-__device__ int last_at_or_below(const int64_t *cum, int n, int64_t v) {  // cum ascending, cum[0] <= v: the last such i
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cum[mid] <= v) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
 // Two ways to share the units out (see latent_attend.hip): pieces of row tiles, a
 // piece a workgroup, where there are fewer row tiles than workgroups and the
 // largest piece is not much above even work; even runs otherwise.
@@ -90,15 +81,12 @@ __device__ void make_plan(const LatentPlan &p, uint8_t *lds) {
     most = max(most, tmp32[4 + w]);
   }
   __syncthreads();
-  auto div_up = [](int64_t x, int64_t y) {  // 64-bit division is slow, and rarely needed
-    return x + y < (1ll << 31) ? (int64_t)(((uint32_t)x + (uint32_t)y - 1) / (uint32_t)y) : (x + y - 1) / y;
-  };
-  const int64_t even = div_up(total, p.n_wg);
+  const int64_t even = latent_div_up(total, p.n_wg);
 
   // the smallest pieces that are no more than the workgroups: 16 sizes at a time, 16 threads a size
   int piece = 0;
   if (n_rows > 0 && n_rows < p.n_wg) {
-    const int64_t size = even + (tid >> 4), top = min(even + min(p.over, 15), div_up(total, p.n_wg - n_rows));
+    const int64_t size = even + (tid >> 4), top = min(even + min(p.over, 15), latent_div_up(total, p.n_wg - n_rows));
     int c = 0;
     if (size <= top)
       for (int b = tid & 15; b < p.a.B; b += 16)
@@ -133,37 +121,22 @@ __device__ void make_plan(const LatentPlan &p, uint8_t *lds) {
     at0 += (int64_t)rr[i] * (piece ? (kk[i] + piece - 1) / piece : kk[i] + over);
   }
   __syncthreads();
-  const int64_t per = piece ? 1 : max(div_up(all, p.n_wg), (int64_t)1);
+  const int64_t per = piece ? 1 : max(latent_div_up(all, p.n_wg), (int64_t)1);
+  // a share is a 32-bit number of units; more, hours of work, is reported and left out
+  const bool fits = per < (int64_t)1 << 31;
+  if (!fits && tid == 0) atomicOr(p.a.err, (uint32_t)ERRF_LATENT);
   int shared0 = 0;
   for (int w0 = 0; w0 < p.n_wg; w0 += 256) {
     const int w = w0 + tid;
     const int64_t v = w * per;
     WgDesc d{};
     TileDesc t{};
-    if (w < p.n_wg && v < all) {
+    if (w < p.n_wg && v < all && fits) {
       // the last sequence that starts at or before v is the one that has it: those without units share their
       // successor's start
-      const int b = last_at_or_below(start, p.a.B, v);
-      const int k = tiles_of(lens[b]);
-      const uint32_t r = (uint32_t)min(v - start[b], (int64_t)0x7fffffff);
+      const int b = latent_last_at_or_below(start, p.a.B, v);
       d = WgDesc{b, 0, 0, 0, t0s[b], nqs[b], lens[b], over};
-      if (piece) {
-        // piece i of c of row tile mt; a piece's row tiles are neighbours, which read the same cache rows
-        const int c = (k + piece - 1) / piece, tiles = rows_of(nqs[b]), i = r / (uint32_t)tiles;
-        d.mt = r % (uint32_t)tiles;
-        d.at = i * (k / c) + min(i, k % c);
-        d.n = k / c + (i < k % c ? 1 : 0);
-        if (i == 0 && c > 1) t = TileDesc{b, d.mt, w, c, tiles, 0};
-      } else {
-        d.mt = r / (uint32_t)(k + over);
-        d.at = r % (uint32_t)(k + over);
-        d.n = (int)min(per, all - v);
-        // shared with the workgroups before, and the first boundary in this row tile
-        const int64_t u0 = v - d.at;
-        const int first = (int)((u0 + over) / per);
-        if (d.at > over && first == w - 1)
-          t = TileDesc{b, d.mt, first, (int)((u0 + over + k - 1) / per) - first + 1, 1, u0};
-      }
+      latent_share(w, v, all, per, piece, over, b, start[b], rows_of(nqs[b]), tiles_of(lens[b]), &d, &t);
     }
     if (w < p.n_wg) p.wg[w] = d;
     int n;

@@ -106,8 +106,8 @@ class LatentAttention:
         projections before norm and rotation, sequence after sequence. tree: the
         tokens' visibility words (ints, bit j: own token j of the sequence) for
         drafts that branch, with depth: each token's distance in positions from
-        its sequence's first new one. Returns [T][H][d_v]. What is refused here
-        leaves the sequences as they were."""
+        its sequence's first new one. Returns [T][H][d_v]. A call that raises leaves
+        the sequences as they were."""
         c = self.cfg
         T = sum(counts)
         if (q.shape[0] != T or kv.shape[0] != T or len(seqs) != len(counts) or len(set(seqs)) != len(seqs) or
@@ -127,6 +127,18 @@ class LatentAttention:
                 for n, b, t in zip(counts, before, itertools.accumulate(counts, initial=0))]
         if max(ends, default=0) > self.turn.shape[0]:
             raise ValueError(f"position {max(ends) - 1} is behind max_positions {self.turn.shape[0]}")
+        try:
+            return self._enqueue(seqs, counts, q, kv, tree, depth, before)
+        except BaseException:
+            # given back in the order that leaves the free pages as they were
+            for s, b in reversed(list(zip(seqs, before))):
+                self._resize(s, b)
+            raise
+
+    def _enqueue(self, seqs, counts, q, kv, tree, depth, before) -> torch.Tensor:
+        """forward after its own checks: the pages of the new tokens, then the calls."""
+        c = self.cfg
+        T = sum(counts)
         start, pos, slot = [0], [], []
         for s, n, b in zip(seqs, counts, before):
             self._resize(s, b + n)

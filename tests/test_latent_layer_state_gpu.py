@@ -1,0 +1,53 @@
+"""The latent-attention layer object's state: refused calls, its own copies of
+the weights, kept drafts, streams, and the choice of form where the expanded
+one cannot run."""
+import numpy as np
+import pytest
+
+from tests.test_latent_layer_gpu import DC, DN, DR, DV, H, close, definition, layer, tokens  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+def causal(n):
+    return np.tril(np.ones((n, n), bool))
+
+
+def state(L):
+    return dict(L._len), {s: list(p) for s, p in L._pages.items()}, list(L._free)
+
+
+def test_calls_refused_after_the_pages_are_taken_leave_the_sequences(layer):
+    """What the entry points refuse (types, shapes, strides, limits) comes back as it was, and the next call is right."""
+    a, b = layer.new_sequence(), layer.new_sequence()
+    q, kv = tokens(40, 120)
+    layer.forward([a], [30], q[:30], kv[:30])
+    before = state(layer)
+
+    def refused(error, *args, **kw):
+        with pytest.raises(error):
+            layer.forward(*args, **kw)
+        assert state(layer) == before
+
+    for n in (2, 90):  # absorbed and expanded
+        x, y = q[30:30 + n], kv[30:30 + n]
+        refused(TypeError, [a], [n], x.float(), y)
+        refused(TypeError, [a], [n], x, y.float())
+        refused(TypeError, [a, b], [n - 1, 1], x.cpu(), y)
+        refused(ValueError, [a], [n], x[:, :H - 1], y)
+        refused(ValueError, [a], [n], x[..., :DN + DR - 8], y)
+        refused(ValueError, [a], [n], x.transpose(1, 2).contiguous().transpose(1, 2), y)
+        refused(ValueError, [a], [n], x, y[:, :DC])
+        wide = torch.zeros((n, DC + DR + 4), dtype=torch.float16, device="cuda")
+        refused(RuntimeError, [a], [n], x, wide[:, :DC + DR])  # rows no multiple of 8 apart
+    many = [layer.new_sequence() for _ in range(1024)]
+    before = state(layer)
+    refused(RuntimeError, [a] + many, [2] + [0] * 1024, q[30:32], kv[30:32])  # 1025 sequences
+    for s in many:
+        layer.drop_sequence(s)
+    out = layer.forward([a], [2], q[30:32], kv[30:32])
+    layer.ctx.check()
+    close(out, definition(layer, q[:32], kv[:32], np.arange(32), causal(32))[30:])
+    layer.drop_sequence(a)
+    layer.drop_sequence(b)

@@ -118,6 +118,8 @@ class LatentAttention:
         if tree is not None and (len(tree) != T or len(depth) != T or max(counts, default=0) > 64 or
                                  any(int(d) < 0 for d in depth)):
             raise ValueError("a word and a depth (from 0) a token, 64 tokens a sequence at most")
+        if tree is not None and any(not 0 <= int(w) < 1 << 64 for w in tree):
+            raise ValueError("a token's word has 64 bits")
         if self.w_kv is None:
             raise RuntimeError("set_weights comes first")
         before = [self._len[s] for s in seqs]

@@ -51,3 +51,15 @@ def test_calls_refused_after_the_pages_are_taken_leave_the_sequences(layer):
     close(out, definition(layer, q[:32], kv[:32], np.arange(32), causal(32))[30:])
     layer.drop_sequence(a)
     layer.drop_sequence(b)
+
+
+@pytest.mark.parametrize("word", [1 << 64, (1 << 64) + 1, -1])
+def test_words_beyond_64_bits_are_refused(layer, word):
+    s = layer.new_sequence()
+    q, kv = tokens(41, 3)
+    layer.forward([s], [1], q[:1], kv[:1])
+    before = state(layer)
+    with pytest.raises(ValueError):
+        layer.forward([s], [2], q[1:], kv[1:], tree=[1, word], depth=[0, 1])
+    assert state(layer) == before
+    layer.drop_sequence(s)

@@ -40,17 +40,25 @@ class LatentAttention:
     # -- weights -----------------------------------------------------------
     def set_weights(self, w_kv, norm_w=None):
         """w_kv [H][d_nope + d_v][d_latent] (a head's key rows, then its value
-        rows), norm_w [d_latent] or None (latents enter the cache as they are)."""
+        rows), norm_w [d_latent] or None (latents enter the cache as they are).
+        The layer keeps copies: what is given may be overwritten or freed after
+        the call."""
         c, stream, caller = self.cfg, self.ctx.stream, torch.cuda.current_stream(self.cache.device)
+        w_kv, norm_w = torch.as_tensor(w_kv), None if norm_w is None else torch.as_tensor(norm_w)
+        shape = (c.n_heads, c.d_nope + c.d_v, c.d_latent)
+        if w_kv.shape != shape:
+            raise ValueError(f"w_kv shape {tuple(w_kv.shape)} != {shape}")
+        if norm_w is not None and norm_w.shape != (c.d_latent,):
+            raise ValueError(f"norm_w shape {tuple(norm_w.shape)} != {(c.d_latent,)}")
         stream.wait_stream(caller)  # the weights may still be on their way there
         with torch.cuda.stream(stream):
-            self.w_kv = torch.as_tensor(w_kv).to(device=self.device, dtype=c.dtype).contiguous()
+            self.w_kv = torch.empty(shape, dtype=c.dtype, device=self.device).copy_(w_kv)
             # the absorbed form's layout of the key rows
             self.w_kt = self.w_kv[:, :c.d_nope].transpose(1, 2).contiguous()
             self.norm_w = None
             if norm_w is not None:
-                self.norm_w = torch.as_tensor(norm_w).to(device=self.device, dtype=torch.float32)
-        caller.wait_stream(stream)  # and may be overwritten or freed after the call
+                self.norm_w = torch.empty(c.d_latent, dtype=torch.float32, device=self.device).copy_(norm_w)
+        caller.wait_stream(stream)
 
     # -- sequences ----------------------------------------------------------
     def new_sequence(self) -> int:

@@ -63,3 +63,34 @@ def test_words_beyond_64_bits_are_refused(layer, word):
         layer.forward([s], [2], q[1:], kv[1:], tree=[1, word], depth=[0, 1])
     assert state(layer) == before
     layer.drop_sequence(s)
+
+
+def test_the_layer_has_its_own_weights():
+    """Tensors that already have the layer's type and place may be overwritten after set_weights, in both forms."""
+    import quantized_moe_expert_sigmoid_amd as moe
+    from quantized_moe_expert_sigmoid_amd.latent import LatentAttention
+    ctx = moe.MoeCtx(0)
+    L = LatentAttention(ctx, H, DC, DR, DN, DV, n_pages=40, page_size=16, max_positions=400, dtype=torch.float16)
+    g = torch.Generator().manual_seed(2)
+    w = (torch.randn((H, DN + DV, DC), generator=g) * DC ** -0.5).half().cuda()
+    norm = (1 + 0.1 * torch.randn((DC,), generator=g)).cuda()
+    w_then, norm_then = w.clone(), norm.clone()
+    L.set_weights(w, norm)
+    w.zero_()
+    norm.zero_()
+    assert torch.equal(L.w_kv, w_then) and torch.equal(L.norm_w, norm_then)
+    q, kv = tokens(42, 102)
+    s = L.new_sequence()
+    assert L.expands([100], [100]) and not L.expands([2], [102])
+    out = torch.cat([L.forward([s], [100], q[:100], kv[:100]), L.forward([s], [2], q[100:], kv[100:])])
+    ctx.check()
+    close(out, definition(L, q, kv, np.arange(102), causal(102)))
+
+    # shapes are checked, and a refused call leaves the weights
+    for bad in ((w_then[:, :DN + DV - 1], None), (w_then[:H - 1], norm_then), (w_then.flatten(0, 1), None),
+                (w_then, norm_then[:-1]), (w_then, norm_then[None])):
+        with pytest.raises(ValueError):
+            L.set_weights(*bad)
+    assert torch.equal(L.w_kv, w_then) and torch.equal(L.norm_w, norm_then)
+    assert torch.equal(L.w_kt, w_then[:, :DN].transpose(1, 2))
+    ctx.close()

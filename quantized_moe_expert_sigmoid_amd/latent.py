@@ -44,7 +44,7 @@ class LatentAttention:
         The layer keeps copies: what is given may be overwritten or freed after
         the call."""
         c, stream, caller = self.cfg, self.ctx.stream, torch.cuda.current_stream(self.cache.device)
-        w_kv, norm_w = torch.as_tensor(w_kv), None if norm_w is None else torch.as_tensor(norm_w)
+        w_kv, norm_w = torch.as_tensor(w_kv).detach(), None if norm_w is None else torch.as_tensor(norm_w).detach()
         shape = (c.n_heads, c.d_nope + c.d_v, c.d_latent)
         if w_kv.shape != shape:
             raise ValueError(f"w_kv shape {tuple(w_kv.shape)} != {shape}")

@@ -94,3 +94,15 @@ def test_the_layer_has_its_own_weights():
     assert torch.equal(L.w_kv, w_then) and torch.equal(L.norm_w, norm_then)
     assert torch.equal(L.w_kt, w_then[:, :DN].transpose(1, 2))
     ctx.close()
+
+
+def test_weights_of_a_trained_module_are_values_only(layer):
+    """Parameters are taken by value: nothing of them is held by the layer's copies."""
+    import quantized_moe_expert_sigmoid_amd as moe
+    from quantized_moe_expert_sigmoid_amd.latent import LatentAttention
+    ctx = moe.MoeCtx(0)
+    L = LatentAttention(ctx, H, DC, DR, DN, DV, n_pages=4, page_size=16, max_positions=64, dtype=torch.float16)
+    L.set_weights(torch.nn.Parameter(layer.w_kv.float()), torch.nn.Parameter(layer.norm_w.clone()))
+    assert torch.equal(L.w_kv, layer.w_kv) and torch.equal(L.norm_w, layer.norm_w)
+    assert not any(t.requires_grad for t in (L.w_kv, L.w_kt, L.norm_w))
+    ctx.close()

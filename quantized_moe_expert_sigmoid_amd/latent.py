@@ -97,6 +97,8 @@ class LatentAttention:
         `nodes` (ascending, a path of the tree), in that order, and drop the others."""
         nodes = list(nodes)
         before = self._len[seq] - n_own
+        if n_own < 0 or before < 0:
+            raise ValueError(f"n_own {n_own} of a sequence of {self._len[seq]} tokens")
         if any(not 0 <= v < n_own for v in nodes) or any(a >= b for a, b in zip(nodes, nodes[1:])):
             raise ValueError(f"nodes must ascend within 0..{n_own - 1}")
         flat = self.cache.view(-1, self.cache.shape[-1])

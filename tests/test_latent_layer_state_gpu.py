@@ -106,3 +106,20 @@ def test_weights_of_a_trained_module_are_values_only(layer):
     assert torch.equal(L.w_kv, layer.w_kv) and torch.equal(L.norm_w, layer.norm_w)
     assert not any(t.requires_grad for t in (L.w_kv, L.w_kt, L.norm_w))
     ctx.close()
+
+
+@pytest.mark.parametrize("n_own", [31, 47, 1000, -1])
+def test_keep_takes_no_more_tokens_than_there_are(layer, n_own):
+    s = layer.new_sequence()
+    q, kv = tokens(43, 31)
+    layer.forward([s], [30], q[:30], kv[:30])
+    before, rows = state(layer), layer.cache.clone()
+    for nodes in ([], [0], [0, 20]):
+        with pytest.raises(ValueError):
+            layer.keep(s, n_own, nodes)
+        assert state(layer) == before
+    assert torch.equal(layer.cache, rows)
+    out = layer.forward([s], [1], q[30:], kv[30:])
+    layer.ctx.check()
+    close(out, definition(layer, q, kv, np.arange(31), causal(31))[30:])
+    layer.drop_sequence(s)

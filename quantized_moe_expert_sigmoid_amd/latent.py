@@ -2,8 +2,11 @@
 
 Every call appends the new tokens (moe_latent_append) and attends to the
 sequences' cached rows: moe_latent_attend for single tokens and drafted trees,
-moe_latent_prompt for prompts. Everything runs on the context's stream; the
-sequences' pages and lengths are kept on the host and sent with each call.
+moe_latent_prompt for prompts. Everything runs on the context's stream. A call
+starts after the work that the caller's current stream holds, and that stream
+waits for the call, so that tensors made and used on it need no further
+ordering. The sequences' pages and lengths are kept on the host and sent with
+each call.
 """
 from __future__ import annotations
 
@@ -164,23 +167,31 @@ class LatentAttention:
         def send(values, dtype):
             return torch.tensor(values, dtype=dtype).to(self.device)
 
+        stream, caller = self.ctx.stream, torch.cuda.current_stream(self.cache.device)
+        out = torch.empty((T, c.n_heads, c.d_v), dtype=c.dtype, device=self.device)  # the caller's memory, its stream's
+        if stream != caller:
+            stream.wait_stream(caller)  # q and kv may still be in the making
         words = None
-        with torch.cuda.stream(self.ctx.stream):
-            if tree is not None:
-                words = send([int(w) - (1 << 64) if int(w) >> 63 else int(w) for w in tree], torch.int64)
-            table, start_d = send(table, torch.int32).view(len(seqs), wide), send(start, torch.int32)
-            kv_len = send([self._len[s] for s in seqs], torch.int32)
-            q_rope = torch.empty((T, c.n_heads, c.d_rope), dtype=c.dtype, device=self.device)
-            out = torch.empty((T, c.n_heads, c.d_v), dtype=c.dtype, device=self.device)
-            moe_latent_append(self.ctx, c, kv, self.turn, send(pos, torch.int32), send(slot, torch.int64), self.cache,
-                              norm_w=self.norm_w, eps=self.eps, q_rope=q[..., c.d_nope:], q_rope_out=q_rope)
-            n_kv = sum(self._len[s] for s in seqs)
-            if tree is None and self.expands(counts, [self._len[s] for s in seqs]):
-                moe_latent_prompt(self.ctx, c, q[..., :c.d_nope], q_rope, self.w_kv, self.cache, table, start_d, kv_len,
-                                  n_kv, out)
-            else:
-                moe_latent_attend(self.ctx, c, q[..., :c.d_nope], q_rope, self.w_kt, self.w_kv, self.cache, table,
-                                  start_d, kv_len, max(counts, default=0), out, tree=words)
+        try:
+            with torch.cuda.stream(stream):
+                if tree is not None:
+                    words = send([int(w) - (1 << 64) if int(w) >> 63 else int(w) for w in tree], torch.int64)
+                table, start_d = send(table, torch.int32).view(len(seqs), wide), send(start, torch.int32)
+                kv_len = send([self._len[s] for s in seqs], torch.int32)
+                q_rope = torch.empty((T, c.n_heads, c.d_rope), dtype=c.dtype, device=self.device)
+                moe_latent_append(self.ctx, c, kv, self.turn, send(pos, torch.int32), send(slot, torch.int64),
+                                  self.cache, norm_w=self.norm_w, eps=self.eps, q_rope=q[..., c.d_nope:],
+                                  q_rope_out=q_rope)
+                n_kv = sum(self._len[s] for s in seqs)
+                if tree is None and self.expands(counts, [self._len[s] for s in seqs]):
+                    moe_latent_prompt(self.ctx, c, q[..., :c.d_nope], q_rope, self.w_kv, self.cache, table, start_d,
+                                      kv_len, n_kv, out)
+                else:
+                    moe_latent_attend(self.ctx, c, q[..., :c.d_nope], q_rope, self.w_kt, self.w_kv, self.cache, table,
+                                      start_d, kv_len, max(counts, default=0), out, tree=words)
+        finally:
+            if stream != caller:
+                caller.wait_stream(stream)  # which may now read out, and overwrite or free q and kv
         return out
 
     def expands(self, counts, lengths) -> bool:

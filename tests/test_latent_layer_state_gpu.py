@@ -123,3 +123,38 @@ def test_keep_takes_no_more_tokens_than_there_are(layer, n_own):
     layer.ctx.check()
     close(out, definition(layer, q, kv, np.arange(31), causal(31))[30:])
     layer.drop_sequence(s)
+
+
+def test_calls_are_ordered_with_the_callers_stream(layer):
+    """A context on a stream of its own, nothing synchronised: q and kv are still being made when forward is called,
+    are overwritten and freed right after it, and its result is read at once."""
+    import quantized_moe_expert_sigmoid_amd as moe
+    from quantized_moe_expert_sigmoid_amd.latent import LatentAttention
+    ctx = moe.MoeCtx(0, torch.cuda.Stream())
+    L = LatentAttention(ctx, H, DC, DR, DN, DV, n_pages=40, page_size=16, max_positions=400, dtype=torch.float16)
+    L.set_weights(layer.w_kv, layer.norm_w)
+    data, caller = tokens(45, 130), torch.cuda.Stream()
+    busy = torch.randn((4096, 4096), device="cuda")
+    torch.cuda.synchronize()
+    counts, outs = [120, 1, 1, 8], []
+    with torch.cuda.stream(caller):
+        s, at = L.new_sequence(), 0
+        for n in counts:
+            x = busy
+            for _ in range(40):  # about 100 ms before the inputs are there
+                x = torch.mm(x, busy).mul_(2.0 ** -6)
+            q, kv = [torch.full_like(d[at:at + n], float("nan")) for d in data]
+            q.copy_(data[0][at:at + n]).add_(x[0, 0] * 0)
+            kv.copy_(data[1][at:at + n]).add_(x[0, 0] * 0)
+            out = L.forward([s], [n], q, kv)
+            q.fill_(float("nan"))
+            kv.fill_(float("nan"))
+            outs.append(out * 1)
+            out.fill_(float("nan"))
+            del q, kv, out
+            at += n
+        got = torch.cat(outs)
+    caller.synchronize()
+    ctx.check()
+    close(got, definition(layer, *data, np.arange(130), causal(130)))
+    ctx.close()

@@ -569,8 +569,9 @@ moe_status moe_latent_attend(moe_ctx *ctx, const moe_latent_cfg *cfg, const moe_
                              const void *w_kv, const uint64_t *tree, int max_q);
 
 /* Expanded form, causal: query i of n sees the rows 0 .. kv_len - n + i. n_kv:
- * at least the sum of kv_len (sizes the expansion's workspace of n_kv *
- * n_heads * (d_nope + d_v) elements; a larger sum is reported by moe_ctx_check
+ * at least the sum of kv_len, at most 2^24 (sizes the expansion's workspace of
+ * n_kv * n_heads * (d_nope + d_v) elements; MOE_ENOMEM, with nothing enqueued,
+ * if that cannot be allocated; a larger sum is reported by moe_ctx_check
  * and the sequences beyond it are not computed). Other arguments and rules as
  * above. */
 moe_status moe_latent_prompt(moe_ctx *ctx, const moe_latent_cfg *cfg, const moe_latent_call *call, const void *w_kv,

@@ -14,7 +14,9 @@ import itertools
 
 import torch
 
-from . import LatentCfg, MoeCtx, moe_latent_append, moe_latent_attend, moe_latent_prompt
+from . import MOE_ENOMEM, LatentCfg, MoeCtx, MoeError, moe_latent_append, moe_latent_attend, moe_latent_prompt
+
+MAX_EXPANDED = 1 << 24  # cached rows that moe_latent_prompt takes
 
 
 class LatentAttention:
@@ -182,11 +184,17 @@ class LatentAttention:
                 moe_latent_append(self.ctx, c, kv, self.turn, send(pos, torch.int32), send(slot, torch.int64),
                                   self.cache, norm_w=self.norm_w, eps=self.eps, q_rope=q[..., c.d_nope:],
                                   q_rope_out=q_rope)
-                n_kv = sum(self._len[s] for s in seqs)
-                if tree is None and self.expands(counts, [self._len[s] for s in seqs]):
-                    moe_latent_prompt(self.ctx, c, q[..., :c.d_nope], q_rope, self.w_kv, self.cache, table, start_d,
-                                      kv_len, n_kv, out)
-                else:
+                lengths = [self._len[s] for s in seqs]
+                expanded = tree is None and self.expands(counts, lengths)
+                if expanded:
+                    try:
+                        moe_latent_prompt(self.ctx, c, q[..., :c.d_nope], q_rope, self.w_kv, self.cache, table,
+                                          start_d, kv_len, sum(lengths), out)
+                    except MoeError as e:
+                        if e.status != MOE_ENOMEM:
+                            raise
+                        expanded = False  # no room for the expanded rows: the other form needs none
+                if not expanded:
                     moe_latent_attend(self.ctx, c, q[..., :c.d_nope], q_rope, self.w_kt, self.w_kv, self.cache, table,
                                       start_d, kv_len, max(counts, default=0), out, tree=words)
         finally:
@@ -195,12 +203,14 @@ class LatentAttention:
         return out
 
     def expands(self, counts, lengths) -> bool:
-        """Whether the expanded form takes fewer products: it pays d_latent
+        """Whether the expanded form can run and takes fewer products: it pays d_latent
         (d_nope + d_v) a cached row to save 2 d_latent - d_nope - d_v a query and
         row. Measured (128 heads, 2000 rows before the call; us expanded,
         absorbed): 64 tokens 133, 85; 128 tokens 139, 123 (absorbed takes 0.84 of
         the products); 256 tokens 153, 190 (1.33)."""
         c = self.cfg
+        if sum(lengths) > MAX_EXPANDED:
+            return False
         pairs = sum(n * (m - n) + n * (n + 1) // 2 for n, m in zip(counts, lengths))
         wide = c.d_latent * (c.d_nope + c.d_v)
         absorbed = pairs * (2 * c.d_latent + c.d_rope) + sum(counts) * wide

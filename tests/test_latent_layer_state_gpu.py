@@ -158,3 +158,39 @@ def test_calls_are_ordered_with_the_callers_stream(layer):
     ctx.check()
     close(got, definition(layer, *data, np.arange(130), causal(130)))
     ctx.close()
+
+
+def test_prompts_beyond_the_expanded_form_are_absorbed(layer, monkeypatch):
+    """More cached rows than moe_latent_prompt takes, or no memory for its workspace: the other form of the same function."""
+    import quantized_moe_expert_sigmoid_amd as moe
+    from quantized_moe_expert_sigmoid_amd import latent
+    assert layer.expands([4096], [1 << 24])
+    assert not layer.expands([4096], [(1 << 24) + 1])
+    assert not layer.expands([4096, 1], [1 << 23, (1 << 23) + 1])
+
+    q, kv = tokens(44, 100)
+    want = definition(layer, q, kv, np.arange(100), causal(100))
+    asked = []
+
+    def full(*args):
+        asked.append(args[-2])
+        raise moe.MoeError(moe.MOE_ENOMEM, "hipMalloc: out of memory")
+
+    monkeypatch.setattr(latent, "moe_latent_prompt", full)
+    s = layer.new_sequence()
+    out = layer.forward([s], [100], q, kv)
+    layer.ctx.check()
+    assert asked == [100]
+    close(out, want)
+    layer.drop_sequence(s)
+
+    def wrong(*args):
+        raise moe.MoeError(moe.MOE_EINVAL, "another error")
+
+    monkeypatch.setattr(latent, "moe_latent_prompt", wrong)
+    s = layer.new_sequence()
+    before = state(layer)
+    with pytest.raises(moe.MoeError):
+        layer.forward([s], [100], q, kv)
+    assert state(layer) == before
+    layer.drop_sequence(s)

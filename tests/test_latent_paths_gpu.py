@@ -119,3 +119,35 @@ def test_trees_in_fp16(moe, ctx, dims):  # noqa: F811
     q, n = [3, 64, 1, 17, 0, 40], [100, 64, 1, 17 + 47, 12, 40 + 130]
     check(Problem(107, q, n, **dims, dtype="fp16", tree=random_tree(rng, q)), moe, ctx, "absorbed",
           heads=[0, dims["H"] // 2, dims["H"] - 1])
+
+
+# --- workspaces of more than 2^32 bytes -------------------------------------------------------
+
+def test_expanded_rows_beyond_32_bits(moe, ctx):  # noqa: F811
+    """2^16 rows of 128 heads, 256 elements each: the last heads' rows lie past 2^32 bytes."""
+    p = Problem(108, [3, 2], [68000, 50], **WIDE, page=64)
+    assert sum(p.n) * p.H * (p.dn + p.dv) * 2 > 2 ** 32
+    check(p, moe, ctx, "expanded", heads=[0, 126, 127])
+
+
+def test_absorbed_queries_beyond_32_bits(moe, ctx):  # noqa: F811
+    """131073 tokens of 128 heads ahead of the tokens that are looked at; their own sequence has no rows."""
+    p = Problem(109, [5, 1], [60, 33], **dict(TINY, H=128))
+    d, many = p.gpu(), 2 ** 17 + 1
+    assert many * p.H * p.dc * 2 > 2 ** 32
+    q = torch.zeros((many + p.T, p.H, p.dn + p.dr), dtype=d["q"].dtype, device="cuda")
+    q[many:] = d["q"]
+    d["q"] = q
+    d["out"] = torch.full((many + p.T, p.H, p.dv), 7.0, dtype=q.dtype, device="cuda")
+    d["q_start"] = torch.tensor([0, many, many + 5, many + 6], dtype=torch.int32, device="cuda")
+    d["kv_len"] = torch.tensor([0, 60, 33], dtype=torch.int32, device="cuda")
+    d["table"] = torch.cat([d["table"][:1], d["table"]]).contiguous()
+    out = p.run(moe, ctx, "absorbed", d, max_q=many)
+    ctx.check()
+    assert not out[:many].any()
+    heads = [0, 127]
+    part = copy.copy(p)
+    part.H, part.q, part.w_kv = 2, p.q[:, heads], p.w_kv[heads]
+    ref, tol = part.reference("absorbed")
+    got = out[many:].double().cpu().numpy()
+    assert np.isfinite(got).all() and (np.abs(got[:, heads] - ref) <= tol).all()

@@ -264,11 +264,6 @@ __device__ __forceinline__ void lds_load16(const void *p, uint32_t to, int on = 
                "s"(to - OFF), "s"(on), "n"(OFF)
                : "memory");
 }
-// The same with a wave's common address and a lane's offset.
-__device__ __forceinline__ void lds_load16_s(const void *base, uint32_t off, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(to)
-               : "memory");
-}
 
 // A sequence's bounds, made safe: tokens [t0, t0 + nq) of the call, len cached
 // rows, the first `before` of them older than the call (negative when the

@@ -85,7 +85,8 @@ struct Attend {
   static constexpr int kBufs = kQL || DC < 512 ? 3 : 4;  // tile buffers: one being read, the others in flight
   static constexpr int kQB = kWaves * kQL * 1024;
   static constexpr int kLds = kBufs * kTileB + kQB;
-  // small rows of few registers: two workgroups a CU, so that one computes while the other starts or ends a run
+  // small rows of few registers: two workgroups a CU, so that one computes while the other starts or ends a run (at
+  // the price of 13 to 18 spilled registers with row tiles of 64 rows for latents of 256, mostly outside the loop)
   static constexpr int kPerCu = DC < 512 && kNB <= 4 ? 2 : 1;
   static_assert(kWaves == 4 && kPerCu * kLds <= 160 << 10, "4 waves load a tile's 32 tokens, 8 each");
 };
@@ -188,7 +189,9 @@ __global__ __launch_bounds__(256, (Attend<DC, DR, WM, WN>::kPerCu)) void latent_
           lds_load16<g * 128>(src, uniform(to + g * C::kPanelB), uniform(on));
       };
 
-      // the first tiles' loads fly while the queries are read
+      // The first tiles' loads are asked for ahead of the queries and fly while those are read. Not so with row tiles of
+      // 64 rows for latents of 512 and 256 and of 128 for 256: the compiler reuses registers between the two and waits
+      // for the tiles before it asks for a query.
       if (s.len > 0)
 #pragma unroll
         for (int i = 0; i < kBufs - 1; ++i) {
@@ -382,8 +385,10 @@ __global__ __launch_bounds__(256, (Attend<DC, DR, WM, WN>::kPerCu)) void latent_
 // fourth partial result, and the waves are joined through LDS. J = 1 is for few
 // row tiles of many partial results, J = 8 for many row tiles (one token over
 // 131072 rows: 22 us with 1, 66 us with 8; 64 tokens over 1000-8000 rows: 26 and
-// 16 us). The bytes are the bound: 67 MB of partial results of 256 workgroups,
-// read in 16 us, 4.2 TB/s; with none it is a launch, 4.6 us.
+// 16 us). The lengths are on the device, so the host chooses by the call's row tiles
+// alone: one sequence of 131072 rows among 16 and among 31 of 500 gets J = 8 and
+// takes 33 and 74 us. The bytes are the bound: 67 MB of partial results of 256
+// workgroups, read in 16 us, 4.2 TB/s; with none it is a launch, 4.6 us.
 constexpr int kFew = 16;
 
 template <typename E, int WM, int J>

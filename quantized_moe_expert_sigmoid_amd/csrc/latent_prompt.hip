@@ -13,10 +13,12 @@
 // double the workspace's bytes (0.0028 relative in bf16, 0.0017 of it the output's
 // own rounding).
 //
-// Measured (128 heads, keys of 128 + 64, values of 128, 4096 tokens): rows 7 us,
-// expansion 163 us (latent_gemm.hip), attention 745 us, 687 GFLOP at 920 TFLOP/s,
-// where the library's product of 8192 x 8192 x 8192 reaches 1350. The products
-// bound it, at the clock (1.7 to 2.1 GHz) that they leave.
+// Measured: 4096 tokens of 128 heads, keys of 128 + 64, values of 128: rows 7 us,
+// expansion 163 us (latent_gemm.hip), attention 745 to 760 us by machine, 687 GFLOP
+// at 915 TFLOP/s; of 64 heads, keys of 192 + 64, values of 256: expansion 143 us,
+// attention 607 us, 550 GFLOP at 905 TFLOP/s, with 25 registers of a lane spilled.
+// The library's product of 8192 x 8192 x 8192 reaches 1350. The products bound it,
+// at the clock (1.7 to 2.1 GHz) that they leave.
 #include "latent.h"
 
 #include <algorithm>

@@ -35,6 +35,9 @@
  *            hardware", section "Key features": attention over a compressed
  *            cache (32,768 -> 576 floats a token) and weight absorption, which
  *            removes the per-token reconstruction of keys and values.
+ *  [OCP-MX]  Open Compute Project, "OCP Microscaling Formats (MX)
+ *            Specification", version 1.0: MXFP4 (blocks of 32 E2M1 values with
+ *            an E8M0 scale) and the conversion to it.
  *  [P-mtp]   tech.takumi3488.com, "Trying colibri", the MTP section: drafted
  *            tokens are verified together.
  *
@@ -502,7 +505,7 @@ int moe_pool_resident(const moe_pool *pool, int layer, int expert);
  * n_heads 1..128; d_latent 128, 256 or 512; d_rope 32 or 64; (d_nope, d_v)
  * (64, 64), (128, 128) or (192, 256); page_size a power of two up to 65536;
  * scale finite. */
-enum { MOE_BF16 = 0, MOE_FP16 = 1 };
+enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 /* where a call says so */ };
 typedef struct {
   int n_heads, d_latent, d_rope, d_nope, d_v;
   int dtype; /* MOE_BF16 or MOE_FP16 */
@@ -576,6 +579,85 @@ moe_status moe_latent_attend(moe_ctx *ctx, const moe_latent_cfg *cfg, const moe_
  * above. */
 moe_status moe_latent_prompt(moe_ctx *ctx, const moe_latent_cfg *cfg, const moe_latent_call *call, const void *w_kv,
                              int64_t n_kv);
+
+/* ---------------------------------------------------------------------- */
+/* Microscaled 4-bit floating point ([OCP-MX], [P-feat])                  */
+/* ---------------------------------------------------------------------- */
+
+/* Matrices kept in 4 bits with a scale for each 32 values, the format that
+ * gfx950's matrix cores multiply as it is. Row r of K values (a multiple of 32,
+ * at most 65536) is K / 2 bytes of codes and K / 32 scale bytes:
+ *   codes [rows][K / 2]: element 2i in the low half of byte i. A code is a sign
+ *     (bit 3) and 0, 0.5, 1, 1.5, 2, 3, 4 or 6 (bits 0 to 2).
+ *   scales [rows][K / 32]: byte s stands for 2^(s - 127), 255 for NaN.
+ * An element is its code's value times its block's scale. Types of unquantised
+ * arrays: MOE_BF16, MOE_FP16 or MOE_FP32.
+ *
+ * Products: every sum is fp32 and rounded once to the result's type. A product
+ * of codes is exact; a block of NaN makes the results it takes part in NaN. */
+
+/* x: rows of K values, row r at x + r * x_t elements (x_t at least K, a multiple
+ * of 4 fp32 or 8 16-bit elements). A block's scale is 2^(floor(log2 max|x|) - 2),
+ * at least 2^-127; its codes are the values over the scale, rounded to the
+ * nearest (ties to the code with bit 0 clear), above 6 to 6. The sign of zero is
+ * kept. A block that holds an infinity or NaN gets scale byte 255 and codes 0.
+ * rows * K at most 2^34. codes must not overlap x. */
+moe_status moe_mx_quantize(moe_ctx *ctx, int dtype, const void *x, int64_t rows, int K, int64_t x_t,
+                           uint8_t *codes, uint8_t *scales);
+/* The values that codes and scales stand for, out [rows][K], rounded to the
+ * type. rows * K at most 2^34. */
+moe_status moe_mx_dequantize(moe_ctx *ctx, int dtype, const uint8_t *codes, const uint8_t *scales, int64_t rows,
+                             int K, void *out);
+
+/* out [M][N] = x w^T: x M rows and w N rows of K values, each given as codes and
+ * scales. M at most 2^22, N at most 2^20. */
+moe_status moe_mx_matmul(moe_ctx *ctx, int dtype, const uint8_t *x, const uint8_t *sx, int64_t M,
+                         const uint8_t *w, const uint8_t *sw, int N, int K, void *out);
+
+/* The product grouped by expert, with ragged sizes ([P-dedup]: an expert's
+ * weights are read once for all its lines). w: E (1..1024) matrices of N rows of K
+ * values, one after another. Line l of L (at most 2^22) belongs to expert e when
+ * offsets[e] <= l < offsets[e + 1] (DEVICE int32 [E + 1], ascending within 0..L;
+ * as moe_bucket_tokens leaves them); lines outside every expert are not computed.
+ * It is row in_rows[l] of x (DEVICE int32 [L]; NULL: row l), and its result goes
+ * to row out_rows[l] of out (DEVICE int32 [L], distinct; NULL: row l). x has X
+ * rows, out R rows of N; rows of out that no line goes to are left as they were.
+ * Offsets that do not ascend within 0..L and rows out of range are reported by
+ * moe_ctx_check as MOE_EINVAL, never read or written (a line whose row is out of
+ * range is not written; with bad offsets the results are unspecified). Nothing is
+ * read on the host: a captured graph may be replayed on other offsets and rows. */
+moe_status moe_mx_grouped_matmul(moe_ctx *ctx, int dtype, const uint8_t *x, const uint8_t *sx, int64_t X,
+                                 const uint8_t *w, const uint8_t *sw, int E, int N, int K, const int32_t *offsets,
+                                 int64_t L, const int32_t *in_rows, const int32_t *out_rows, void *out, int64_t R);
+
+/* One expert's weights in 4 bits: device pointers, codes 16-byte aligned.
+ * gate, up: I rows of H values; down: H rows of I. */
+typedef struct {
+  const uint8_t *gate, *up, *down;
+  const uint8_t *s_gate, *s_up, *s_down;
+} moe_mx_expert_w;
+
+/* One expert as a single contiguous block, in the order of moe_mx_expert_w, each
+ * part starting on a 256-byte boundary: writes the six byte offsets to
+ * offsets_host[6] (nullable) and returns the block's bytes, or 0 when H or I is
+ * not a positive multiple of 64. Host-only. */
+size_t moe_mx_expert_layout(int H, int I, size_t *offsets_host);
+
+/* The experts' FFN on hidden states x [T][H] and the combine, in one call:
+ *   out[t] = FFN_E(t) (with has_shared) + sum_j topk_w[t][j] FFN_e(t), e =
+ *   topk_idx[t][j];  FFN(t) = down q(silu(gate q(x[t])) * (up q(x[t]))),
+ * q: to 4 bits as moe_mx_quantize does it. silu(g) = g / (1 + exp(-g)) in fp32 as
+ * in moe_expert_ffn_q4; the slots' results are fp32 (MOE_BF16: rounded to bf16)
+ * and summed in fp32, the shared expert's first, then in slot order.
+ * experts: DEVICE array [E], or [E + 1] with has_shared, whose last entry is the
+ * shared expert. x and out (not the same array) are of type dtype. topk_idx int32
+ * and topk_w fp32 [T][k] as moe_router_topk gives them. Slots of weight 0 or id
+ * -1 add nothing; any other id outside [0, E), or an id repeated within one
+ * token's slots (the later one), adds nothing either and is reported by
+ * moe_ctx_check. Limits of T, H, I, E and k as for moe_expert_ffn_q4. */
+moe_status moe_expert_ffn_mx(moe_ctx *ctx, int dtype, const moe_mx_expert_w *experts, int has_shared,
+                             const void *x, const int32_t *topk_idx, const float *topk_w, int T, int H, int I,
+                             int E, int k, void *out);
 
 /* ---------------------------------------------------------------------- */
 /* Measurement                                                            */

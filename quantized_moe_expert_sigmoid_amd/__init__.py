@@ -127,6 +127,13 @@ _SIGS = {
                                  _i64, _vp, _i64, _i64, _vp]),
     "moe_latent_attend": (_i32, [_vp, ctypes.POINTER(_LatentCfg), ctypes.POINTER(_LatentCall), _vp, _vp, _vp, _i32]),
     "moe_latent_prompt": (_i32, [_vp, ctypes.POINTER(_LatentCfg), ctypes.POINTER(_LatentCall), _vp, _i64]),
+    "moe_mx_quantize": (_i32, [_vp, _i32, _vp, _i64, _i32, _i64, _vp, _vp]),
+    "moe_mx_dequantize": (_i32, [_vp, _i32, _vp, _vp, _i64, _i32, _vp]),
+    "moe_mx_matmul": (_i32, [_vp, _i32, _vp, _vp, _i64, _vp, _vp, _i32, _i32, _vp]),
+    "moe_mx_grouped_matmul": (_i32, [_vp, _i32, _vp, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp,
+                                     _i64]),
+    "moe_mx_expert_layout": (_sz, [_i32, _i32, ctypes.POINTER(_sz)]),
+    "moe_expert_ffn_mx": (_i32, [_vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp]),
 }
 
 
@@ -567,6 +574,126 @@ def moe_latent_prompt(ctx: MoeCtx, cfg: LatentCfg, q_nope: torch.Tensor, q_rope:
 
 
 # ---------------------------------------------------------------------------
+# Microscaled 4-bit floating point
+# ---------------------------------------------------------------------------
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _dtype(t: torch.Tensor, name):
+    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be a bfloat16, float16 or float32 tensor")
+    return _DTYPES[t.dtype]
+
+
+def _on(ctx: MoeCtx, t: torch.Tensor, dtype, name, shape=None):
+    """_dev, on the context's device."""
+    p = _dev(t, dtype, name, shape)
+    if t.device.index != ctx.device:
+        raise ValueError(f"{name} is on {t.device}, the context on device {ctx.device}")
+    return p
+
+
+def _mx(ctx, codes, scales, name):
+    """A matrix as codes [..., K / 2] and scales [..., K / 32]: (codes' address, scales', K)."""
+    c = _on(ctx, codes, torch.uint8, f"{name} codes")
+    K = 2 * codes.shape[-1]
+    if K % 32:
+        raise ValueError(f"{name} codes: rows of {K} values are no whole blocks of 32")
+    return c, _on(ctx, scales, torch.uint8, f"{name} scales", (*codes.shape[:-1], K // 32)), K
+
+
+def moe_mx_quantize(ctx: MoeCtx, x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
+    """Rows to 4 bits (see include/moe.h): x [rows][K], bfloat16, float16 or
+    float32 (rows may be strided), codes uint8 [rows][K / 2], scales uint8
+    [rows][K / 32]."""
+    dtype = _dtype(x, "x")
+    if not x.is_cuda or x.device.index != ctx.device:
+        raise TypeError(f"x must be on device {ctx.device}")
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be [rows][K] with contiguous rows")
+    rows, K = x.shape
+    if K % 32:
+        raise ValueError(f"x: rows of {K} values are no whole blocks of 32")
+    _ck(lib().moe_mx_quantize(ctx.handle, dtype, x.data_ptr(), rows, K, x.stride(0) if rows > 1 else K,
+                              _on(ctx, codes, torch.uint8, "codes", (rows, K // 2)),
+                              _on(ctx, scales, torch.uint8, "scales", (rows, K // 32))))
+    return codes, scales
+
+
+def moe_mx_dequantize(ctx: MoeCtx, codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor):
+    """What codes [rows][K / 2] and scales [rows][K / 32] stand for, in out
+    [rows][K] (bfloat16, float16 or float32)."""
+    c, s, K = _mx(ctx, codes, scales, "")
+    if codes.dim() != 2:
+        raise ValueError("codes must be [rows][K / 2]")
+    rows = codes.shape[0]
+    _ck(lib().moe_mx_dequantize(ctx.handle, _dtype(out, "out"), c, s, rows, K,
+                                _on(ctx, out, out.dtype, "out", (rows, K))))
+    return out
+
+
+def moe_mx_matmul(ctx: MoeCtx, x: torch.Tensor, sx: torch.Tensor, w: torch.Tensor, sw: torch.Tensor,
+                  out: torch.Tensor):
+    """out [M][N] = x w^T (see include/moe.h): codes x [M][K / 2] and w [N][K / 2]
+    with their scales; out bfloat16, float16 or float32."""
+    xp, sxp, K = _mx(ctx, x, sx, "x")
+    wp, swp, Kw = _mx(ctx, w, sw, "w")
+    if x.dim() != 2 or w.dim() != 2 or K != Kw:
+        raise ValueError(f"x {tuple(x.shape)} and w {tuple(w.shape)} must be [M][K / 2] and [N][K / 2]")
+    M, N = x.shape[0], w.shape[0]
+    _ck(lib().moe_mx_matmul(ctx.handle, _dtype(out, "out"), xp, sxp, M, wp, swp, N, K,
+                            _on(ctx, out, out.dtype, "out", (M, N))))
+    return out
+
+
+def moe_mx_grouped_matmul(ctx: MoeCtx, x: torch.Tensor, sx: torch.Tensor, w: torch.Tensor, sw: torch.Tensor,
+                          offsets: torch.Tensor, out: torch.Tensor, in_rows: torch.Tensor | None = None,
+                          out_rows: torch.Tensor | None = None):
+    """The product grouped by expert (see include/moe.h): codes x [X][K / 2], w
+    [E][N][K / 2], offsets int32 [E + 1], out [R][N]; in_rows and out_rows int32
+    [lines]: each line's row of x and of out (None: its own number). Without
+    either there are as many lines as the smaller of X and R."""
+    xp, sxp, K = _mx(ctx, x, sx, "x")
+    wp, swp, Kw = _mx(ctx, w, sw, "w")
+    if x.dim() != 2 or w.dim() != 3 or K != Kw:
+        raise ValueError(f"x {tuple(x.shape)} and w {tuple(w.shape)} must be [X][K / 2] and [E][N][K / 2]")
+    (E, N), X, R = w.shape[:2], x.shape[0], out.shape[0]
+    L = min(X, R) if in_rows is None and out_rows is None else (out_rows if in_rows is None else in_rows).shape[0]
+    ip = None if in_rows is None else _on(ctx, in_rows, torch.int32, "in_rows", (L,))
+    op = None if out_rows is None else _on(ctx, out_rows, torch.int32, "out_rows", (L,))
+    _ck(lib().moe_mx_grouped_matmul(ctx.handle, _dtype(out, "out"), xp, sxp, X, wp, swp, E, N, K,
+                                    _on(ctx, offsets, torch.int32, "offsets", (E + 1,)), L, ip, op,
+                                    _on(ctx, out, out.dtype, "out", (R, N)), R))
+    return out
+
+
+def moe_expert_ffn_mx(ctx: MoeCtx, table: torch.Tensor, has_shared: bool, x: torch.Tensor, topk_idx: torch.Tensor,
+                      topk_w: torch.Tensor, I: int, out: torch.Tensor):
+    """The experts' FFN in 4 bits with the combine (see include/moe.h): table
+    int64 [E][6] of moe_mx_expert_w (with has_shared a further row, the shared
+    expert), x and out [T][H] of one type (bfloat16, float16 or float32),
+    topk_idx int32 and topk_w float32 [T][k]."""
+    T, H = x.shape
+    k = topk_idx.shape[1]
+    rows = table.shape[0]
+    _ck(lib().moe_expert_ffn_mx(ctx.handle, _dtype(x, "x"), _on(ctx, table, torch.int64, "experts table", (rows, 6)),
+                                1 if has_shared else 0, _on(ctx, x, x.dtype, "x"),
+                                _on(ctx, topk_idx, torch.int32, "topk_idx", (T, k)),
+                                _on(ctx, topk_w, torch.float32, "topk_w", (T, k)), T, H, I,
+                                rows - (1 if has_shared else 0), k, _on(ctx, out, x.dtype, "out", (T, H))))
+    return out
+
+
+def moe_mx_expert_layout(H: int, I: int):
+    offs = (ctypes.c_size_t * 6)()
+    n = lib().moe_mx_expert_layout(H, I, offs)
+    if n == 0:
+        raise MoeError(MOE_EINVAL, f"moe_mx_expert_layout: H {H} I {I}")
+    return int(n), [int(o) for o in offs]
+
+
+# ---------------------------------------------------------------------------
 # Expert storage helpers (device memory via torch, layout from the library)
 # ---------------------------------------------------------------------------
 
@@ -604,6 +731,31 @@ class ExpertBlocks:
         moe_quantize_rows(ctx, self.bits, wg, g, sg)
         moe_quantize_rows(ctx, self.bits, wu, u, su)
         moe_quantize_rows(ctx, self.bits, wd, d, sd)
+
+
+class MxExpertBlocks:
+    """n experts in 4 bits, stored as contiguous blocks (moe_mx_expert_layout)
+    in one device tensor, plus the device table of moe_mx_expert_w pointers."""
+
+    def __init__(self, n: int, H: int, I: int, device="cuda"):
+        self.n, self.H, self.I = n, H, I
+        self.block_bytes, self.offsets = moe_mx_expert_layout(H, I)
+        self.data = torch.empty((n, self.block_bytes), dtype=torch.uint8, device=device)
+        base = self.data.data_ptr()
+        rows = [[base + e * self.block_bytes + o for o in self.offsets] for e in range(n)]
+        self.table = torch.tensor(rows, dtype=torch.int64, device=device)
+
+    def views(self, e: int):
+        """(gate, up, down, s_gate, s_up, s_down) tensor views of expert e."""
+        H, I = self.H, self.I
+        shapes = [(I, H // 2), (I, H // 2), (H, I // 2), (I, H // 32), (I, H // 32), (H, I // 32)]
+        return [self.data[e, o:o + r * c].view(r, c) for o, (r, c) in zip(self.offsets, shapes)]
+
+    def pack_from_fp32(self, ctx: MoeCtx, e: int, wg: torch.Tensor, wu: torch.Tensor, wd: torch.Tensor):
+        """Quantise gate, up and down (float32, or 16-bit) on the GPU straight into expert e's block."""
+        v = self.views(e)
+        for i, w in enumerate((wg, wu, wd)):
+            moe_mx_quantize(ctx, w, v[i], v[3 + i])
 
 
 # ---------------------------------------------------------------------------

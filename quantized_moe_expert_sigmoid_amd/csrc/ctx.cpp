@@ -266,6 +266,8 @@ extern "C" moe_status moe_ctx_check(moe_ctx *ctx) {
     if (flags & ERRF_LATENT)
       return moe_fail(MOE_EINVAL, "device: latent attention: page, slot, position or sequence bound out of range "
                       "(flags 0x%x)", flags);
+    if (flags & ERRF_MX)
+      return moe_fail(MOE_EINVAL, "device: grouped product: offsets or a line's row out of range (flags 0x%x)", flags);
     return moe_fail(MOE_EINVAL, "device: error flags 0x%x", flags);
   }
   return MOE_OK;

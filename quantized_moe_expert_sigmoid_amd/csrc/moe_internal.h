@@ -19,6 +19,7 @@ enum : uint32_t {
   ERRF_TIMEOUT = 1u << 1,    // a bounded wait gave up
   ERRF_RANGE = 1u << 2,      // an int32 accumulator bound was exceeded
   ERRF_LATENT = 1u << 3,     // latent attention: a page, slot, position or sequence bound out of range
+  ERRF_MX = 1u << 4,         // 4-bit products: offsets or a line's row out of range
 };
 
 struct moe_ctx {

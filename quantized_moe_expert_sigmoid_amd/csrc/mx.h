@@ -1,0 +1,182 @@
+// Shared by the kernels on microscaled 4-bit floating point (mx*.hip, mx.cpp).
+//
+// A row of K values is K / 32 blocks; a block has one scale byte s, worth
+// 2^(s - 127) (255: not a number), and 32 codes of 4 bits, two a byte, the
+// first in the low half: sign, then 0, 0.5, 1, 1.5, 2, 3, 4 or 6. So a block's
+// codes are 16 bytes, what one lane gives to a matrix instruction.
+#pragma once
+
+#include "moe_internal.h"
+
+constexpr int kMxBlock = 32;
+
+// A product's arrays as the kernels see them (device pointers).
+struct MxProduct {
+  const uint8_t *x, *sx;  // codes and scales of X rows of K values
+  int64_t X;
+  // weights, N rows of K values an expert: expert e's at w + e * w_e ..., or where table says
+  const uint8_t *w, *sw;
+  int64_t w_e, sw_e;
+  const moe_mx_expert_w *table;
+  int N, K;
+  // lines: line l is row in_rows[l] / k of x (NULL: l) and goes to row out_rows[l] of out (NULL: l)
+  const int32_t *offsets;  // [E + 1], expert e's lines are offsets[e] ..; NULL: one expert has all L of them
+  int E;
+  int64_t L;
+  const int32_t *in_rows, *out_rows;
+  int k;
+  int64_t shared;  // lines L .. L + shared - 1 are expert E's; with in_rows they are rows 0 .. of x, else rows L ..
+  void *out;
+  int64_t R;  // rows of out
+  uint32_t *err;
+};
+
+moe_status launch_mx_quantize(moe_ctx *ctx, int dtype, const void *x, int64_t rows, int K, int64_t x_t,
+                              uint8_t *codes, uint8_t *scales);
+moe_status launch_mx_dequantize(moe_ctx *ctx, int dtype, const uint8_t *codes, const uint8_t *scales, int64_t rows,
+                                int K, void *out);
+// out = x w^T line by line
+moe_status launch_mx_product(moe_ctx *ctx, int dtype, const MxProduct &p);
+// silu(x gate^T) * (x up^T) line by line (the table's gate and up), in 4 bits: out's row l is line l
+moe_status launch_mx_gateup(moe_ctx *ctx, const MxProduct &p, uint8_t *scales);
+// the table's down
+moe_status launch_mx_down(moe_ctx *ctx, int dtype, const MxProduct &p);
+moe_status launch_mx_combine(moe_ctx *ctx, int y_dtype, int dtype, const void *y, const int32_t *idx, const float *w,
+                             int T, int k, int E, int H, int has_shared, void *out);
+
+#if defined(__HIPCC__)
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+
+// Results' types: four fp32 values rounded once (to nearest even) and stored together.
+template <int DTYPE>
+struct MxOut;
+template <>
+struct MxOut<MOE_FP32> {
+  typedef float T;
+  typedef f32x4 V;
+  static __device__ __forceinline__ V of(f32x4 v) { return v; }
+  static __device__ __forceinline__ T one(float v) { return v; }
+  static __device__ __forceinline__ float back(T v) { return v; }
+};
+template <>
+struct MxOut<MOE_BF16> {
+  typedef __bf16 T;
+  typedef bf16x4 V;
+  static __device__ __forceinline__ V of(f32x4 v) { return __builtin_convertvector(v, bf16x4); }
+  static __device__ __forceinline__ T one(float v) { return (__bf16)v; }
+  static __device__ __forceinline__ float back(T v) { return (float)v; }
+};
+template <>
+struct MxOut<MOE_FP16> {
+  typedef _Float16 T;
+  typedef f16x4 V;
+  static __device__ __forceinline__ V of(f32x4 v) { return __builtin_convertvector(v, f16x4); }
+  static __device__ __forceinline__ T one(float v) { return (_Float16)v; }
+  static __device__ __forceinline__ float back(T v) { return (float)v; }
+};
+
+// The scale byte of a block whose largest |x| has these bits: the largest value
+// comes to lie in [4, 8); values above 6 become 6. Zero and the smallest
+// numbers get the smallest scale, an infinity or NaN anywhere the byte 255.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
+  const uint32_t e = top >> 23;
+  return e == 255 ? 255u : e < 2 ? 0u : e - 2;
+}
+// 2^(s - 127), s < 255
+__device__ __forceinline__ float mx_scale_value(uint32_t s) { return __uint_as_float(s ? s << 23 : 0x400000u); }
+
+// c += a b^T with v_mfma_scale_f32_16x16x128_f8f6f4: lane l holds block l / 16 (of four) of row l % 16 of a and of b and
+// in the low bytes of sa and sb these blocks' scales; of c it holds column l % 16 (b's row), rows 4 (l / 16) + i.
+__device__ __forceinline__ f32x4 mx_mfma16(i32x4 a, int sa, i32x4 b, int sb, f32x4 c) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1),
+                                                          __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1), c,
+                                                          4, 4, 0, sa, 0, sb);
+}
+
+// A unit of work: up to `tile` lines of one expert.
+struct MxUnit {
+  int e;           // expert; E for the shared one
+  int64_t first;   // its first line
+  int n;           // lines; 0: no such unit
+};
+__device__ __forceinline__ int mx_uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t mx_uniform(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)mx_uniform((int)(v >> 32)) << 32 | (uint32_t)mx_uniform((int)v));
+}
+
+// Unit u of the lines in tiles: the shared expert's tiles first, then each
+// expert's, in order. Every wave finds its unit by itself, in one round trip
+// to memory: a lane counts the tiles of E / 64 experts in a row, a scan over
+// the wave's lanes and a ballot name the lane. Offsets that do not ascend
+// within 0 .. L are reported and cut to that range.
+template <int TILE>
+__device__ __forceinline__ MxUnit mx_unit(const MxProduct &p, int64_t u) {
+  const int64_t s = (p.shared + TILE - 1) / TILE;
+  if (u < s) return MxUnit{p.E, p.L + u * TILE, (int)min((int64_t)TILE, p.shared - u * TILE)};
+  u -= s;
+  if (!p.offsets) {
+    const int64_t left = p.L - u * TILE;
+    return MxUnit{0, u * TILE, (int)max((int64_t)0, min((int64_t)TILE, left))};
+  }
+  const int lane = threadIdx.x & 63, per = (p.E + 63) / 64, e0 = min(lane * per, p.E), e1 = min(e0 + per, p.E);
+  const int top = (int)min(p.L, (int64_t)INT32_MAX);
+  bool ok = true;
+  auto at = [&](int e) {
+    const int o = p.offsets[e];
+    ok &= o >= 0 && o <= top;
+    return min(max(o, 0), top);
+  };
+  int tiles = 0, lo = at(e0);
+  const int first_lo = lo;
+  for (int e = e0; e < e1; ++e) {
+    const int hi = at(e + 1);
+    ok &= hi >= lo;
+    tiles += (max(hi - lo, 0) + TILE - 1) / TILE;
+    lo = max(hi, lo);
+  }
+  if (!ok) atomicOr(p.err, (uint32_t)ERRF_MX);
+  int sum = tiles;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(sum, o, 64);
+    if (lane >= o) sum += v;
+  }
+  const uint64_t past = __ballot((int64_t)sum > u);
+  if (!past) return MxUnit{0, 0, 0};
+  const int who = __ffsll((unsigned long long)past) - 1;
+  // that lane's experts once more, now all lanes alike
+  int left = (int)u - __shfl(sum - tiles, who, 64), base = __shfl(first_lo, who, 64);
+  for (int e = who * per;; ++e) {
+    const int hi = max(base, min(max(p.offsets[e + 1], 0), top)), n = (hi - base + TILE - 1) / TILE;
+    if (left < n || e + 1 >= min((who + 1) * per, p.E)) {
+      const int first = base + left * TILE;
+      return MxUnit{mx_uniform(e), mx_uniform(first), mx_uniform(max(0, min(TILE, hi - first)))};
+    }
+    left -= n;
+    base = hi;
+  }
+}
+
+// Row of x of a line, and where its result goes; -1: out of range, which is reported.
+__device__ __forceinline__ int64_t mx_in_row(const MxProduct &p, int64_t line) {
+  int64_t r = line;
+  if (p.in_rows) r = line < p.L ? p.in_rows[line] / p.k : line - p.L;
+  if (r >= 0 && r < p.X) return r;
+  atomicOr(p.err, (uint32_t)ERRF_MX);
+  return -1;
+}
+__device__ __forceinline__ int64_t mx_out_row(const MxProduct &p, int64_t line) {
+  const int64_t r = line < p.L && p.out_rows ? p.out_rows[line] : line;
+  if (r >= 0 && r < p.R) return r;
+  atomicOr(p.err, (uint32_t)ERRF_MX);
+  return -1;
+}
+
+#endif  // __HIPCC__

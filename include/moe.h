@@ -630,7 +630,7 @@ moe_status moe_mx_grouped_matmul(moe_ctx *ctx, int dtype, const uint8_t *x, cons
                                  const uint8_t *w, const uint8_t *sw, int E, int N, int K, const int32_t *offsets,
                                  int64_t L, const int32_t *in_rows, const int32_t *out_rows, void *out, int64_t R);
 
-/* One expert's weights in 4 bits: device pointers, codes 16-byte aligned.
+/* One expert's weights in 4 bits: device pointers, 16-byte aligned.
  * gate, up: I rows of H values; down: H rows of I. */
 typedef struct {
   const uint8_t *gate, *up, *down;

@@ -62,8 +62,8 @@ static moe_status product_check(const char *fn, moe_ctx *ctx, int dtype, const M
           "%s: %lld lines, %lld rows of x, %lld of out", fn, (long long)p.L, (long long)p.X, (long long)p.R);
   if (p.L == 0 || p.N == 0) return MOE_OK;
   REQUIRE(p.x && p.sx && p.w && p.sw && p.out, "%s: NULL pointer", fn);
-  REQUIRE(moe_aligned16(p.x) && moe_aligned16(p.w) && moe_aligned16(p.out),
-          "%s: x, w and out must be 16-byte aligned", fn);
+  REQUIRE(moe_aligned16(p.x) && moe_aligned16(p.w) && moe_aligned16(p.sx) && moe_aligned16(p.sw) && moe_aligned16(p.out),
+          "%s: x, w, their scales and out must be 16-byte aligned", fn);
   return MOE_OK;
 }
 

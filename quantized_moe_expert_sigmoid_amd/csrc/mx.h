@@ -126,11 +126,21 @@ __device__ __forceinline__ int64_t mx_uniform(int64_t v) {
   return (int64_t)((uint64_t)(uint32_t)mx_uniform((int)(v >> 32)) << 32 | (uint32_t)mx_uniform((int)v));
 }
 
+// Inclusive sums over the wave's lanes.
+__device__ __forceinline__ int mx_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // from 1, 2, 4, 8 lanes before, within 16
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // lane 15 of the 16 before, lane 31
+  return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+}
+
 // Unit u of the lines in tiles: the shared expert's tiles first, then each
 // expert's, in order. Every wave finds its unit by itself, in one round trip
-// to memory: a lane counts the tiles of E / 64 experts in a row, a scan over
-// the wave's lanes and a ballot name the lane. Offsets that do not ascend
-// within 0 .. L are reported and cut to that range.
+// to memory: a lane counts the tiles of E / 64 experts in a row (at most 16), a
+// scan over the wave's lanes and a ballot name the lane. Offsets that do not
+// ascend within 0 .. L are reported and cut to that range.
 template <int TILE>
 __device__ __forceinline__ MxUnit mx_unit(const MxProduct &p, int64_t u) {
   const int64_t s = (p.shared + TILE - 1) / TILE;
@@ -140,43 +150,42 @@ __device__ __forceinline__ MxUnit mx_unit(const MxProduct &p, int64_t u) {
     const int64_t left = p.L - u * TILE;
     return MxUnit{0, u * TILE, (int)max((int64_t)0, min((int64_t)TILE, left))};
   }
-  const int lane = (int)(threadIdx.x & 63), per = (p.E + 63) / 64, e0 = min(lane * per, p.E), e1 = min(e0 + per, p.E);
-  const int top = (int)min(p.L, (int64_t)INT32_MAX);
-  bool ok = true;
-  auto at = [&](int e) {
-    const int o = p.offsets[e];
-    ok &= o >= 0 && o <= top;
-    return min(max(o, 0), top);
-  };
-  int tiles = 0, lo = at(e0);
-  const int first_lo = lo;
-  for (int e = e0; e < e1; ++e) {
-    const int hi = at(e + 1);
-    ok &= hi >= lo;
-    tiles += (max(hi - lo, 0) + TILE - 1) / TILE;
-    lo = max(hi, lo);
-  }
-  if (!ok) atomicOr(p.err, (uint32_t)ERRF_MX);
-  int sum = tiles;
+  const int lane = (int)(threadIdx.x & 63), per = (p.E + 63) / 64, e0 = lane * per;
+  const int top = (int)p.L;
+  int v[17];  // offsets of this lane's experts, the next lane's first one last
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int v = __shfl_up(sum, o, 64);
-    if (lane >= o) sum += v;
-  }
+  for (int c = 0; c < 4; ++c)
+    if (c == 0 || 4 * c < per) {  // all lanes alike
+      if (c == 0) v[0] = p.offsets[min(e0, p.E)];
+#pragma unroll
+      for (int i = 1; i <= 4; ++i) v[4 * c + i] = p.offsets[min(e0 + min(4 * c + i, per), p.E)];
+    }
+  bool ok = v[0] >= 0 && v[0] <= top;
+  v[0] = min(max(v[0], 0), top);
+  int tiles = 0;
+#pragma unroll
+  for (int i = 1; i <= 16; ++i)
+    if (i <= 4 || (i + 3) / 4 * 4 - 4 < per) {
+      ok &= v[i] >= v[i - 1] && v[i] <= top;
+      v[i] = max(v[i - 1], min(v[i], top));
+      tiles += (v[i] - v[i - 1] + TILE - 1) / TILE;
+    }
+  if (!ok) atomicOr(p.err, (uint32_t)ERRF_MX);
+  const int sum = mx_scan(tiles);
   const uint64_t past = __ballot((int64_t)sum > u);
   if (!past) return MxUnit{0, 0, 0};
   const int who = __ffsll((unsigned long long)past) - 1;
-  // that lane's experts once more, now all lanes alike
-  int left = (int)u - __shfl(sum - tiles, who, 64), base = __shfl(first_lo, who, 64);
-  for (int e = who * per;; ++e) {
-    const int hi = max(base, min(max(p.offsets[e + 1], 0), top)), n = (hi - base + TILE - 1) / TILE;
-    if (left < n || e + 1 >= min((who + 1) * per, p.E)) {
-      const int first = base + left * TILE;
-      return MxUnit{mx_uniform(e), mx_uniform(first), mx_uniform(max(0, min(TILE, hi - first)))};
+  int left = (int)u - __builtin_amdgcn_readlane(sum - tiles, who), lo = __builtin_amdgcn_readlane(v[0], who);
+  MxUnit r{0, 0, 0};
+#pragma unroll
+  for (int i = 1; i <= 16; ++i)
+    if ((i <= 4 || (i + 3) / 4 * 4 - 4 < per) && r.n == 0) {
+      const int hi = __builtin_amdgcn_readlane(v[i], who), n = (hi - lo + TILE - 1) / TILE;
+      if (left < n) r = MxUnit{who * per + i - 1, lo + left * TILE, min(TILE, hi - lo - left * TILE)};
+      left -= n;
+      lo = hi;
     }
-    left -= n;
-    base = hi;
-  }
+  return r;
 }
 
 // Row of x of a line, and where its result goes; -1: out of range, which is reported.

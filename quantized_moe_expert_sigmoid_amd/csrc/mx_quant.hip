@@ -99,41 +99,40 @@ moe_status dequantize(moe_ctx *ctx, const uint8_t *codes, const uint8_t *scales,
 
 // out[t] = y_shared[t] + sum_j w[t][j] y[t][j], fused multiply-adds in fp32 in slot order, rounded once. Slots of zero
 // weight and slots whose id is no expert, or one that an earlier slot of the token has, are left out unread. y: the
-// T * k slots in order, then the shared expert's T rows.
+// T * k slots in order, then the shared expert's T rows. A workgroup's threads have one token, so that ids and weights
+// are scalars; every slot's values are loaded before the first is used.
 template <int Y, int DTYPE>
 __global__ __launch_bounds__(256) void mx_combine_kernel(const typename MxOut<Y>::T *y, const int32_t *idx,
                                                          const float *w, int T, int k, int E, int H, int has_shared,
                                                          typename MxOut<DTYPE>::T *out) {
   typedef typename MxOut<Y>::V V;
-  const int h4 = H / 4;
-  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int t = (int)(q / h4);
-  if (t >= T) return;
-  const int hh = (int)(q - (int64_t)t * h4) * 4;
   constexpr int kMaxK = 16;
-  float wv[kMaxK];
+  const int per = (H / 4 + 255) / 256;
+  const int64_t t = blockIdx.x / per;
+  const int h = (int)(blockIdx.x % per * 256 + threadIdx.x) * 4;
+  if (h >= H) return;
+  bool used[kMaxK];
   V v[kMaxK], sh = {};
-  if (has_shared) sh = *reinterpret_cast<const V *>(y + ((int64_t)T * k + t) * H + hh);
-  int ids[kMaxK];
+  if (has_shared) sh = *reinterpret_cast<const V *>(y + (T * (int64_t)k + t) * H + h);
 #pragma unroll
   for (int j = 0; j < kMaxK; ++j) {
-    if (j >= k) break;
-    ids[j] = idx[(int64_t)t * k + j];
-    wv[j] = w[(int64_t)t * k + j];
-    v[j] = *reinterpret_cast<const V *>(y + ((int64_t)t * k + j) * H + hh);
+    used[j] = false;
+    if (j < k) {
+      const int id = idx[t * k + j];
+      used[j] = w[t * k + j] != 0.0f && id >= 0 && id < E;
+      for (int i = 0; i < j; ++i) used[j] &= idx[t * k + i] != id;
+      if (used[j]) v[j] = *reinterpret_cast<const V *>(y + (t * k + j) * H + h);
+    }
   }
   f32x4 acc = {(float)sh[0], (float)sh[1], (float)sh[2], (float)sh[3]};
 #pragma unroll
-  for (int j = 0; j < kMaxK; ++j) {
-    if (j >= k) break;
-    bool used = wv[j] != 0.0f && ids[j] >= 0 && ids[j] < E;
+  for (int j = 0; j < kMaxK; ++j)
+    if (used[j]) {
+      const float f = w[t * k + j];
 #pragma unroll
-    for (int i = 0; i < j; ++i) used &= ids[i] != ids[j];
-    if (!used) continue;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(wv[j], (float)v[j][c], acc[c]);
-  }
-  *reinterpret_cast<typename MxOut<DTYPE>::V *>(out + (int64_t)t * H + hh) = MxOut<DTYPE>::of(acc);
+      for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(f, (float)v[j][c], acc[c]);
+    }
+  *reinterpret_cast<typename MxOut<DTYPE>::V *>(out + t * H + h) = MxOut<DTYPE>::of(acc);
 }
 
 template <int Y, int DTYPE>
@@ -142,7 +141,7 @@ void combine(moe_ctx *ctx, const void *y, const int32_t *idx, const float *w, in
   typedef typename MxOut<Y>::T TY;
   typedef typename MxOut<DTYPE>::T TO;
   moe_launch(ctx, MOE_STAGE_COMBINE, mx_combine_kernel<Y, DTYPE>,
-             dim3((unsigned)(((int64_t)T * (H / 4) + 255) / 256)), dim3(256), static_cast<const TY *>(y), idx, w, T, k,
+             dim3((unsigned)(T * ((H / 4 + 255) / 256))), dim3(256), static_cast<const TY *>(y), idx, w, T, k,
              E, H, has_shared, static_cast<TO *>(out));
 }
 

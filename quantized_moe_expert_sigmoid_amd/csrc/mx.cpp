@@ -70,21 +70,7 @@ static moe_status product_check(const char *fn, moe_ctx *ctx, int dtype, const M
 // The product by the kernels that its lines call for.
 static moe_status product_run(moe_ctx *ctx, int dtype, MxProduct &p) {
   p.err = ctx->dev_small;
-  if (!mx_tiles(p.L, p.E)) return launch_mx_product(ctx, dtype, p);
-  p.sx_t = p.sw_t = mx_scale_row(p.K);
-  if (mx_padded(p.K)) {
-    MoeLayout l;
-    const size_t o_x = l.take(p.X * p.sx_t), o_w = l.take((size_t)p.E * p.N * p.sw_t);
-    void *scr = nullptr;
-    moe_status st = moe_scratch(ctx, l.size, &scr);
-    if (st) return st;
-    uint8_t *b = static_cast<uint8_t *>(scr);
-    if ((st = launch_mx_pad_scales(ctx, p.sx, nullptr, 0, p.X, 1, p.K, b + o_x))) return st;
-    if ((st = launch_mx_pad_scales(ctx, p.sw, nullptr, 0, p.N, p.E, p.K, b + o_w))) return st;
-    p.sx = b + o_x, p.sw = b + o_w;
-  }
-  p.sw_e = p.N * p.sw_t;
-  return launch_mx_tile_product(ctx, dtype, p);
+  return mx_tiles(p.L, p.E) ? launch_mx_tile_product(ctx, dtype, p) : launch_mx_product(ctx, dtype, p);
 }
 
 extern "C" moe_status moe_mx_matmul(moe_ctx *ctx, int dtype, const uint8_t *x, const uint8_t *sx, int64_t M,
@@ -149,17 +135,11 @@ extern "C" moe_status moe_expert_ffn_mx(moe_ctx *ctx, int dtype, const moe_mx_ex
   // beside the weights is theirs); fp16 ones are not, since a slot may pass fp16's range where the sum does not
   const int y_dtype = dtype == MOE_BF16 ? MOE_BF16 : MOE_FP32;
   const int64_t routed = (int64_t)T * k, lines = routed + (has_shared ? T : 0);
-  const bool tiles = mx_tiles(lines, E), pad_h = tiles && mx_padded(H), pad_i = tiles && mx_padded(I);
-  const int n_experts = E + (has_shared ? 1 : 0);
   MoeLayout l;
   const size_t o_x = l.take((size_t)T * H / 2), o_sx = l.take((size_t)T * H / kMxBlock), o_counts = l.take(4 * E),
                o_offsets = l.take(4 * (E + 1)), o_perm = l.take(4 * routed), o_a = l.take((size_t)lines * I / 2),
                o_sa = l.take((size_t)lines * I / kMxBlock),
                o_y = l.take((size_t)lines * H * (y_dtype == MOE_BF16 ? 2 : 4));
-  const int64_t row_h = mx_scale_row(H), row_i = mx_scale_row(I);
-  const size_t o_px = l.take(pad_h ? T * row_h : 0), o_pg = l.take(pad_h ? n_experts * I * row_h : 0),
-               o_pu = l.take(pad_h ? n_experts * I * row_h : 0), o_pa = l.take(pad_i ? lines * row_i : 0),
-               o_pd = l.take(pad_i ? n_experts * H * row_i : 0);
   void *scr = nullptr;
   if ((st = moe_scratch(ctx, l.size, &scr))) return st;
   uint8_t *b = static_cast<uint8_t *>(scr);
@@ -171,22 +151,9 @@ extern "C" moe_status moe_expert_ffn_mx(moe_ctx *ctx, int dtype, const moe_mx_ex
   p.x = b + o_x, p.sx = b + o_sx, p.X = T, p.table = experts, p.N = I, p.K = H;
   p.offsets = offsets, p.E = E, p.L = routed, p.in_rows = perm, p.k = k, p.shared = has_shared ? T : 0;
   p.out = b + o_a, p.R = lines, p.err = ctx->dev_small;
-  p.sx_t = p.sw_t = row_h;
-  if (pad_h) {
-    if ((st = launch_mx_pad_scales(ctx, p.sx, nullptr, 0, T, 1, H, b + o_px))) return st;
-    if ((st = launch_mx_pad_scales(ctx, nullptr, experts, 3, I, n_experts, H, b + o_pg))) return st;
-    if ((st = launch_mx_pad_scales(ctx, nullptr, experts, 4, I, n_experts, H, b + o_pu))) return st;
-    p.sx = b + o_px, p.sw = b + o_pg, p.sw2 = b + o_pu, p.sw_e = I * row_h;
-  }
-  if ((st = tiles ? launch_mx_tile_gateup(ctx, p, b + o_sa) : launch_mx_gateup(ctx, p, b + o_sa))) return st;
+  if ((st = launch_mx_gateup(ctx, p, b + o_sa))) return st;
   p.x = b + o_a, p.sx = b + o_sa, p.X = lines, p.N = H, p.K = I;
   p.in_rows = nullptr, p.k = 1, p.out_rows = perm, p.out = b + o_y;
-  p.sx_t = p.sw_t = row_i, p.sw = p.sw2 = nullptr;
-  if (pad_i) {
-    if ((st = launch_mx_pad_scales(ctx, p.sx, nullptr, 0, lines, 1, I, b + o_pa))) return st;
-    if ((st = launch_mx_pad_scales(ctx, nullptr, experts, 5, H, n_experts, I, b + o_pd))) return st;
-    p.sx = b + o_pa, p.sw = b + o_pd, p.sw_e = H * row_i;
-  }
-  if ((st = tiles ? launch_mx_tile_down(ctx, y_dtype, p) : launch_mx_down(ctx, y_dtype, p))) return st;
+  if ((st = launch_mx_down(ctx, y_dtype, p))) return st;
   return launch_mx_combine(ctx, y_dtype, dtype, b + o_y, topk_idx, topk_w, T, k, E, H, has_shared, out);
 }

@@ -18,10 +18,6 @@ struct MxProduct {
   const uint8_t *w, *sw;
   int64_t w_e, sw_e;
   const moe_mx_expert_w *table;
-  // the tile kernels read scales by whole words: a row's scales are sx_t and sw_t bytes apart, multiples of four; with a
-  // table whose own rows are not, sw and, for up, sw2 hold the experts' scales with such rows (see mx_padded)
-  int64_t sx_t, sw_t;
-  const uint8_t *sw2;
   int N, K;
   // lines: line l is row in_rows[l] / k of x (NULL: l) and goes to row out_rows[l] of out (NULL: l)
   const int32_t *offsets;  // [E + 1], expert e's lines are offsets[e] ..; NULL: one expert has all L of them
@@ -41,17 +37,9 @@ moe_status launch_mx_dequantize(moe_ctx *ctx, int dtype, const uint8_t *codes, c
                                 int K, void *out);
 // Whether a product of this many lines over E experts goes to the tile kernels.
 bool mx_tiles(int64_t lines, int E);
-// Rows of scales with room for whole words; the weights' scales of `experts` experts come from s, one after another, or
-// from member `part` (0..5) of the table's entries.
-static inline bool mx_padded(int K) { return K % (4 * kMxBlock) != 0; }
-static inline int64_t mx_scale_row(int K) { return (K / kMxBlock + 3) / 4 * 4; }
-moe_status launch_mx_pad_scales(moe_ctx *ctx, const uint8_t *s, const moe_mx_expert_w *table, int part, int64_t rows,
-                                int experts, int K, uint8_t *out);
 // out = x w^T line by line
 moe_status launch_mx_product(moe_ctx *ctx, int dtype, const MxProduct &p);
 moe_status launch_mx_tile_product(moe_ctx *ctx, int dtype, const MxProduct &p);
-moe_status launch_mx_tile_gateup(moe_ctx *ctx, const MxProduct &p, uint8_t *scales);
-moe_status launch_mx_tile_down(moe_ctx *ctx, int dtype, const MxProduct &p);
 // silu(x gate^T) * (x up^T) line by line (the table's gate and up), in 4 bits: out's row l is line l
 moe_status launch_mx_gateup(moe_ctx *ctx, const MxProduct &p, uint8_t *scales);
 // the table's down

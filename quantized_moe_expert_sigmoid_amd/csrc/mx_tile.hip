@@ -2,23 +2,30 @@
 // lines an expert.
 //
 // C^T (n x m) = W X^T with v_mfma_scale_f32_32x32x64_f8f6f4. A workgroup takes BM
-// lines of one expert and BN rows of weights; steps of 128 k, 64 bytes a row and
-// one word of four scale bytes, come by asynchronous loads. A row's four units of
-// 16 bytes lie at unit ^ (row / 4 % 4), so that the 16 rows of a read meet
-// different banks. Half l / 32 of a wave takes units 2 (l / 32) and the next, so
-// that a lane's two scale bytes of a step are neighbours and the instruction picks
-// one of them.
+// lines of one expert and BN rows of weights; stages of KU blocks of 32 k (4 or 8),
+// 16 KU bytes a row, come by asynchronous loads. A row's units of 16 bytes lie at
+// unit ^ swz(row), so that the 16 rows of a read meet different banks. Half l / 32 of
+// a wave takes units KU / 2 (l / 32) and the next ones, so that a lane's scales of a
+// stage are neighbours.
+//
+// Scales come 16 bytes a row for every 16 / KU stages where rows of scales are
+// multiples of 16 bytes (a stage's own 8 bytes of each row were a third of all
+// requests: 2047 tokens grouped over 256 experts 1074 us so and 925 us with 16); a
+// lane reads the word it needs and the instruction picks a byte. Other rows' scales
+// come a byte a lane, each into a word of its own.
 //
 // A wave has the operands of the next product step in registers before the
 // present one begins, and a stage's place is loaded again while its last products
 // run: STAGES - 1 stages are in flight.
+#include <type_traits>
+
 #include "mx.h"
 
 namespace {
 
 __device__ __attribute__((aligned(16))) const uint8_t mx_zeros[16] = {};
 
-// 16 or 4 bytes a lane from global memory straight into LDS, in order of lanes from byte `to` on; on: -1, or 0 for a load
+// 16 bytes a lane from global memory straight into LDS, in order of lanes from byte `to` on; on: -1, or 0 for a load
 // that moves nothing but is counted all the same. In assembly so that the compiler does not wait for it; the kernel waits
 // by count (vmcnt). All lanes must be active.
 __device__ __forceinline__ void lds_load16(const void *p, uint32_t to, int on) {
@@ -26,13 +33,23 @@ __device__ __forceinline__ void lds_load16(const void *p, uint32_t to, int on) {
                "global_load_lds_dwordx4 %0, off\n\ts_mov_b64 exec, -1" ::"v"(p), "s"(to), "s"(on)
                : "memory");
 }
-__device__ __forceinline__ void lds_load4(const void *p, uint32_t to, int on) {
+// The same for a byte a lane, each into a word.
+__device__ __forceinline__ void lds_load1(const void *p, uint32_t to, int on) {
   asm volatile("s_mov_b32 m0, %1\n\ts_mov_b32 exec_lo, %2\n\ts_mov_b32 exec_hi, %2\n\t"
-               "global_load_lds_dword %0, off\n\ts_mov_b64 exec, -1" ::"v"(p), "s"(to), "s"(on)
+               "global_load_lds_ubyte %0, off\n\ts_mov_b64 exec, -1" ::"v"(p), "s"(to), "s"(on)
                : "memory");
 }
 // s_waitcnt vmcnt(n) alone
 #define WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (((n) >> 4) << 14) | (7 << 4) | (15 << 8))
+
+// f(integral_constant<int, A>) .. f(integral_constant<int, B - 1>)
+template <int A, int B, typename F>
+__device__ __forceinline__ void static_for(F &&f) {
+  if constexpr (A < B) {
+    f(std::integral_constant<int, A>{});
+    static_for<A + 1, B>(f);
+  }
+}
 
 // c += a b^T: lane l holds 32 k of row l % 32 of a and of b, block l / 32 of two, and byte S of sa and sb is its scale; of
 // c it holds column l % 32 (b's row), rows 8 (i / 4) + 4 (l / 32) + i % 4.
@@ -61,15 +78,19 @@ unsigned tile_grid(const TileMap &m) {
   return (unsigned)((blocks + 7) / 8 * 8 * m.g * m.gn);
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES, int OCC, int MODE, int DTYPE>
+template <int BM, int BN, int WM, int WN, int KU, int STAGES, int OCC, bool WIDE, int MODE, int DTYPE>
 __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, TileMap map, uint8_t *a_scales) {
   typedef MxOut<DTYPE> O;
   constexpr int kWaves = WM * WN, FM = BM / WM / 32, FN = BN / WN / 32;
-  constexpr int kRows = BM + BN, kStage = kRows * 64, kScales = kRows * 4;
-  constexpr int kLoads = kRows / 16 / kWaves, kLoadsS = (kRows / 64 + kWaves - 1) / kWaves, kPer = kLoads + kLoadsS;
+  constexpr int kRows = BM + BN, kRowB = KU * 16, kStage = kRows * kRowB, kAt = STAGES * kStage;
+  // scales: stages of a load, loads kept, bytes of one
+  constexpr int kChunk = WIDE ? 16 / KU : 1, kChunks = (STAGES + kChunk - 2) / kChunk + 1, kScales = kRows * (WIDE ? 16 : 4 * KU);
+  constexpr int kRowsL = 64 / KU, kRowsS = WIDE ? 64 : 64 / KU;  // rows of a load instruction, of codes and of scales
+  constexpr int kLoads = kRows / kRowsL / kWaves, kLoadsS = (kRows / kRowsS + kWaves - 1) / kWaves, kPer = kLoads + kLoadsS;
   constexpr int kCols = MODE == kGateUp ? BN / 2 : BN;  // of the result
-  static_assert(BM % 64 == 0 && BN % 64 == 0 && kRows % (16 * kWaves) == 0);
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * (kStage + kScales)];
+  static_assert(kRows % (kRowsL * kWaves) == 0 && kWaves * kRowsL % 16 == 0 && (KU == 4 || KU == 8));
+  static_assert(MODE != kGateUp || FN % 2 == 0 || (FN == 1 && WN % 2 == 0));
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * kStage + kChunks * kScales];
 
   const int xcd = blockIdx.x & 7, j0 = blockIdx.x >> 3, per_block = map.g * map.gn;
   const int block = j0 / per_block * 8 + xcd, rest = j0 % per_block, across = (map.n_tiles + map.gn - 1) / map.gn;
@@ -81,6 +102,8 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
   const int lane = threadIdx.x & 63, wave = mx_uniform((int)(threadIdx.x >> 6)), l32 = lane & 31, hl = lane >> 5;
   const int wm = wave % WM, wn = wave / WM;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
+  // of a row's KU units unit c lies at c ^ swz(row): 256 bytes hold 16 / KU rows
+  auto swz = [](int row) { return KU == 4 ? row >> 2 & 3 : (row >> 1 & 1) << 2 | (row >> 2 & 3); };
 
   const uint8_t *w[2], *sw[2];
   if constexpr (MODE == kPlain) {
@@ -88,13 +111,12 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
     sw[0] = sw[1] = p.sw + u.e * p.sw_e;
   } else if constexpr (MODE == kDown) {
     w[0] = w[1] = p.table[u.e].down;
-    sw[0] = sw[1] = p.sw ? p.sw + u.e * p.sw_e : p.table[u.e].s_down;
+    sw[0] = sw[1] = p.table[u.e].s_down;
   } else {
     w[0] = p.table[u.e].gate, w[1] = p.table[u.e].up;
-    sw[0] = p.sw ? p.sw + u.e * p.sw_e : p.table[u.e].s_gate;
-    sw[1] = p.sw ? p.sw2 + u.e * p.sw_e : p.table[u.e].s_up;
+    sw[0] = p.table[u.e].s_gate, sw[1] = p.table[u.e].s_up;
   }
-  const int blocks = p.K / kMxBlock, steps = (blocks + 3) / 4, full = blocks / 4;
+  const int blocks = p.K / kMxBlock, steps = (blocks + KU - 1) / KU, full = blocks / KU;
   // sources: row r of the tile, the lines first, then the weights' rows (gate's, then up's)
   auto row_of = [&](int r, int &which) -> int64_t {
     if (r < BM) return max(mx_in_row(p, u.first + min(r, u.n - 1)), (int64_t)0);
@@ -102,33 +124,38 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
     which = MODE == kGateUp && n >= kCols;
     return min(n0 + n - which * kCols, p.N - 1);
   };
-  const int mine = (lane & 3) ^ (lane >> 4 & 3);  // the unit of its row that a lane loads
+  const int mine = (lane % KU) ^ swz((wave * kRowsL + lane / KU) & 15);  // the unit of its row that a lane loads
   const uint8_t *src[kLoads], *src_s[kLoadsS];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int r = (i * kWaves + wave) * 16 + (lane >> 2);
+    const int r = (i * kWaves + wave) * kRowsL + lane / KU;
     int which = 0;
     const int64_t row = row_of(r, which);
     src[i] = (r < BM ? p.x : w[which]) + (row * blocks + mine) * 16;
   }
 #pragma unroll
   for (int i = 0; i < kLoadsS; ++i) {
-    const int r = min((i * kWaves + wave) * 64, kRows - 64) + lane;
+    const int r = min((i * kWaves + wave) * kRowsS, kRows - kRowsS) + (WIDE ? lane : lane / KU);
     int which = 0;
     const int64_t row = row_of(r, which);
-    src_s[i] = r < BM ? p.sx + row * p.sx_t : sw[which] + row * p.sw_t;
+    src_s[i] = (r < BM ? p.sx : sw[which]) + row * blocks + (WIDE ? 0 : lane % KU);
   }
   auto load = [&](int s) {
-    const uint32_t to = lds0 + s % STAGES * kStage + wave * 1024, to_s = lds0 + STAGES * kStage + s % STAGES * kScales;
-    const int on = mx_uniform(s < steps ? -1 : 0);
-    const bool there = s < full || 4 * s + mine < blocks;  // behind a row's end zeros
+    const uint32_t to = lds0 + s % STAGES * kStage + wave * 1024, to_s = lds0 + kAt + s / kChunk % kChunks * kScales;
+    const int on = mx_uniform(s < steps ? -1 : 0), on_s = s % kChunk ? 0 : on;
+    // behind a row's end zeros
+    const bool there = s < full || KU * s + mine < blocks, there_s = s < full || KU * s + lane % KU < blocks;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      lds_load16(there ? src[i] + s * 64 : mx_zeros, mx_uniform((int)(to + i * kWaves * 1024)), on);
+      lds_load16(there ? src[i] + s * kRowB : mx_zeros, mx_uniform((int)(to + i * kWaves * 1024)), on);
 #pragma unroll
     for (int i = 0; i < kLoadsS; ++i) {
-      const int r = (i * kWaves + wave) * 64;
-      lds_load4(src_s[i] + s * 4, mx_uniform((int)(to_s + min(r, kRows - 64) * 4)), mx_uniform(r < kRows ? on : 0));
+      const int r = (i * kWaves + wave) * kRowsS;
+      const uint32_t to_r = mx_uniform((int)(to_s + min(r, kRows - kRowsS) * (kScales / kRows)));
+      if constexpr (WIDE)
+        lds_load16(src_s[i] + s * KU, to_r, mx_uniform(r < kRows ? on_s : 0));
+      else
+        lds_load1(there_s ? src_s[i] + s * KU : mx_zeros, to_r, mx_uniform(r < kRows ? on_s : 0));
     }
   };
 #pragma unroll
@@ -140,57 +167,66 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
 #pragma unroll
     for (int j = 0; j < FM; ++j) acc[i][j] = f32x16{};
 
-  // a lane's places: rows l32 of 32, unit 2 hl + k
-  int row_x[FM], row_w[FN], off[2];
+  // a lane's places: rows l32 of 32, units KU / 2 hl + k
+  int row_x[FM], row_w[FN], off[KU / 2];
 #pragma unroll
   for (int j = 0; j < FM; ++j) row_x[j] = (wm * FM + j) * 32;
 #pragma unroll
   for (int i = 0; i < FN; ++i)
-    row_w[i] = BM + (MODE == kGateUp ? (i < FN / 2 ? wn * FN / 2 + i : (BN / 64) + wn * FN / 2 + i - FN / 2) : wn * FN + i) * 32;
+    row_w[i] = BM + (MODE == kGateUp && FN > 1 ? (i < FN / 2 ? wn * FN / 2 + i : (BN / 64) + wn * FN / 2 + i - FN / 2) : wn * FN + i) * 32;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) off[k] = l32 * 64 + (((2 * hl + k) ^ (l32 >> 2 & 3)) << 4);
+  for (int k = 0; k < KU / 2; ++k) off[k] = l32 * kRowB + (((KU / 2 * hl + k) ^ swz(l32 & 15)) << 4);
 
   i32x4 xf[2][FM], wf[2][FN];
-  int xs[2][FM], ws[2][FN];
+  // a stage's scales: a word of bytes, or a word for each product step
+  typedef int Words __attribute__((ext_vector_type(KU / 2)));
+  typedef typename std::conditional<!WIDE, Words, typename std::conditional<KU == 8, int, uint16_t>::type>::type Scale;
+  Scale xs[2][FM], ws[2][FN];
   auto read = [&](int s, int k) {  // operands of product step k of stage s
     const uint8_t *b = lds + s % STAGES * kStage + off[k];
 #pragma unroll
-    for (int i = 0; i < FN; ++i) wf[k][i] = *reinterpret_cast<const i32x4 *>(b + row_w[i] * 64);
+    for (int i = 0; i < FN; ++i) wf[k & 1][i] = *reinterpret_cast<const i32x4 *>(b + row_w[i] * kRowB);
 #pragma unroll
-    for (int j = 0; j < FM; ++j) xf[k][j] = *reinterpret_cast<const i32x4 *>(b + row_x[j] * 64);
+    for (int j = 0; j < FM; ++j) xf[k & 1][j] = *reinterpret_cast<const i32x4 *>(b + row_x[j] * kRowB);
   };
-  auto read_scales = [&](int s) {
-    const uint8_t *b = lds + STAGES * kStage + s % STAGES * kScales + l32 * 4 + 2 * hl;
+  auto read_scales = [&](int s, int to) {
+    constexpr int kRowS = kScales / kRows;
+    const uint8_t *b = lds + kAt + s / kChunk % kChunks * kScales + l32 * kRowS;
+    b += WIDE ? s % kChunk * KU + KU / 2 * hl : 2 * KU * hl;
 #pragma unroll
-    for (int i = 0; i < FN; ++i) ws[s & 1][i] = *reinterpret_cast<const uint16_t *>(b + row_w[i] * 4);
+    for (int i = 0; i < FN; ++i) ws[to][i] = *reinterpret_cast<const Scale *>(b + row_w[i] * kRowS);
 #pragma unroll
-    for (int j = 0; j < FM; ++j) xs[s & 1][j] = *reinterpret_cast<const uint16_t *>(b + row_x[j] * 4);
+    for (int j = 0; j < FM; ++j) xs[to][j] = *reinterpret_cast<const Scale *>(b + row_x[j] * kRowS);
   };
   WAIT_VM((STAGES - 1) * kPer);
   asm volatile("s_barrier" ::: "memory");
   read(0, 0);
-  read_scales(0);
-  auto stage = [&](int s, auto odd) {
-    constexpr int P = decltype(odd)::value;
-    read(s, 1);
-    __builtin_amdgcn_sched_barrier(0);
+  read_scales(0, 0);
+  auto stage = [&](int s, auto parity) {
+    constexpr int P = decltype(parity)::value;
+    static_for<0, KU / 2>([&](auto kc) {
+      constexpr int k = decltype(kc)::value;
+      if constexpr (k + 1 < KU / 2) {
+        read(s, k + 1);
+      } else {  // this stage is read, the next one is there, for every wave
+        WAIT_VM((STAGES - 2) * kPer);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        read(s + 1, 0);
+        read_scales(s + 1, 1 - P);
+        load(s + STAGES);
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < FN; ++i)
+      for (int i = 0; i < FN; ++i)
 #pragma unroll
-      for (int j = 0; j < FM; ++j) acc[i][j] = mfma32<0>(wf[0][i], ws[P][i], xf[0][j], xs[P][j], acc[i][j]);
-    // this stage is read, the next one is there, for every wave
-    __builtin_amdgcn_sched_barrier(0);
-    WAIT_VM((STAGES - 2) * kPer);
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    read(s + 1, 0);
-    read_scales(s + 1);
-    load(s + STAGES);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < FN; ++i)
-#pragma unroll
-      for (int j = 0; j < FM; ++j) acc[i][j] = mfma32<1>(wf[1][i], ws[P][i], xf[1][j], xs[P][j], acc[i][j]);
-    __builtin_amdgcn_sched_barrier(0);
+        for (int j = 0; j < FM; ++j) {
+          if constexpr (WIDE)
+            acc[i][j] = mfma32<k>(wf[k & 1][i], ws[P][i], xf[k & 1][j], xs[P][j], acc[i][j]);
+          else
+            acc[i][j] = mfma32<0>(wf[k & 1][i], ws[P][i][k], xf[k & 1][j], xs[P][j][k], acc[i][j]);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    });
   };
   for (int s = 0; s < steps; s += 2) {
     stage(s, std::integral_constant<int, 0>{});
@@ -199,18 +235,43 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
   WAIT_VM(0);
 
   if constexpr (MODE == kGateUp) {
+    // gate and up of the same rows meet in one wave: they are there, or up's wave hands its own over through LDS
+    constexpr int kPairs = FN > 1 ? FN / 2 : 1;
+    f32x16 up[kPairs][FM];
+    if constexpr (FN > 1) {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) up[i][j] = acc[i + FN / 2][j];
+    } else {
+      __syncthreads();  // every wave has read its last stage
+      f32x4 *box = reinterpret_cast<f32x4 *>(lds) + (wn % (WN / 2) * WM + wm) * FM * 4 * 64 + lane;
+      if (wn >= WN / 2) {
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            box[(4 * j + g) * 64] = f32x4{acc[0][j][4 * g], acc[0][j][4 * g + 1], acc[0][j][4 * g + 2], acc[0][j][4 * g + 3]};
+      }
+      __syncthreads();
+      if (wn >= WN / 2) return;
+#pragma unroll
+      for (int j = 0; j < FM; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) up[0][j][e] = box[(4 * j + e / 4) * 64][e % 4];
+    }
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
       const int m = row_x[j] + l32;
       const int64_t line = u.first + min(m, u.n - 1);
 #pragma unroll
-      for (int i = 0; i < FN / 2; ++i) {
+      for (int i = 0; i < kPairs; ++i) {
         const int n = n0 + row_w[i] - BM;
         float a[16];
         uint32_t top = 0;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          a[e] = moe_silu_f32(acc[i][j][e]) * acc[i + FN / 2][j][e];
+          a[e] = moe_silu_f32(acc[i][j][e]) * up[i][j][e];
           top = max(top, __float_as_uint(a[e]) & 0x7fffffffu);
         }
         // the other half of the wave has the block's other 16 values
@@ -267,27 +328,12 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
   }
 }
 
-// blockIdx.y: the expert.
-__global__ __launch_bounds__(256) void mx_pad_scales_kernel(const uint8_t *s, const moe_mx_expert_w *table, int part,
-                                                            int64_t rows, int blocks, int per, uint32_t *out) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * per) return;
-  const uint8_t *from = table ? (&table[blockIdx.y].gate)[part] : s + blockIdx.y * rows * blocks;
-  const int64_t row = i / per;
-  const int b = (int)(i - row * per) * 4;
-  uint32_t v = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (b + e < blocks) v |= (uint32_t)from[row * blocks + b + e] << (8 * e);
-  out[blockIdx.y * rows * per + i] = v;
-}
-
-template <int BM, int BN, int WM, int WN, int STAGES, int OCC, int MODE, int DTYPE>
+template <int BM, int BN, int WM, int WN, int KU, int STAGES, int OCC, bool WIDE, int MODE, int DTYPE>
 void run(moe_ctx *ctx, const MxProduct &p, uint8_t *a_scales) {
   const int64_t units = (p.offsets ? (p.L < p.E ? p.L : p.L / BM + p.E) : (p.L + BM - 1) / BM) + (p.shared + BM - 1) / BM;
   const int cols = MODE == kGateUp ? BN / 2 : BN;
   const TileMap m = tile_map(units, (p.N + cols - 1) / cols);
-  auto kernel = mx_tile_kernel<BM, BN, WM, WN, STAGES, OCC, MODE, DTYPE>;
+  auto kernel = mx_tile_kernel<BM, BN, WM, WN, KU, STAGES, OCC, WIDE, MODE, DTYPE>;
   if (MODE == kPlain)
     hipLaunchKernelGGL(kernel, dim3(tile_grid(m)), dim3(WM * WN * 64), 0, ctx->stream, p, m, a_scales);
   else
@@ -295,47 +341,58 @@ void run(moe_ctx *ctx, const MxProduct &p, uint8_t *a_scales) {
                m, a_scales);
 }
 
-template <int MODE, int DTYPE>
+#ifndef T1
+#define T1 32
+#define T2 128
+#endif
+// Stages: as many as the LDS holds (a byte's word beside the codes: fewer).
+template <bool WIDE, int MODE, int DTYPE>
 void pick(moe_ctx *ctx, const MxProduct &p, uint8_t *a_scales) {
   const int64_t lines = p.offsets ? p.L / p.E : p.L;
-  if (lines > 128)
-    run<256, 256, 2, 4, 4, 2, MODE, DTYPE>(ctx, p, a_scales);
+  if (lines > T2)
+    run<256, 256, 2, 4, 4, 4, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales);
+  else if (lines > T1)
+    run<128, 256, 2, 4, 8, WIDE ? 3 : 2, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales);
   else
-    run<64, 256, 1, 4, 3, 2, MODE, DTYPE>(ctx, p, a_scales);
+    run<32, 128, 1, 4, 8, 3, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales);
+}
+template <int MODE, int DTYPE>
+void launch(moe_ctx *ctx, const MxProduct &p, uint8_t *a_scales) {
+  if (p.K % (16 * kMxBlock) == 0)
+    pick<true, MODE, DTYPE>(ctx, p, a_scales);
+  else
+    pick<false, MODE, DTYPE>(ctx, p, a_scales);
 }
 
 }  // namespace
 
-moe_status launch_mx_pad_scales(moe_ctx *ctx, const uint8_t *s, const moe_mx_expert_w *table, int part, int64_t rows,
-                                int experts, int K, uint8_t *out) {
-  const int blocks = K / kMxBlock, per = (blocks + 3) / 4;
-  hipLaunchKernelGGL(mx_pad_scales_kernel, dim3((unsigned)((rows * per + 255) / 256), experts), dim3(256), 0,
-                     ctx->stream, s, table, part, rows, blocks, per, reinterpret_cast<uint32_t *>(out));
-  MOE_CHECK_LAUNCH("mx_pad_scales_kernel");
-  return MOE_OK;
-}
-
-bool mx_tiles(int64_t lines, int E) { return lines > 16 * (int64_t)E; }
+#ifdef FORCE_STREAM
+bool mx_tiles(int64_t, int) { return false; }
+#elif defined(FORCE_TILE)
+bool mx_tiles(int64_t, int) { return true; }
+#else
+bool mx_tiles(int64_t lines, int E) { return E > 1 || lines > 16; }
+#endif
 
 moe_status launch_mx_tile_product(moe_ctx *ctx, int dtype, const MxProduct &p) {
   switch (dtype) {
-    case MOE_FP32: pick<kPlain, MOE_FP32>(ctx, p, nullptr); break;
-    case MOE_BF16: pick<kPlain, MOE_BF16>(ctx, p, nullptr); break;
-    default: pick<kPlain, MOE_FP16>(ctx, p, nullptr); break;
+    case MOE_FP32: launch<kPlain, MOE_FP32>(ctx, p, nullptr); break;
+    case MOE_BF16: launch<kPlain, MOE_BF16>(ctx, p, nullptr); break;
+    default: launch<kPlain, MOE_FP16>(ctx, p, nullptr); break;
   }
   MOE_CHECK_LAUNCH("mx tile kernel");
   return MOE_OK;
 }
-moe_status launch_mx_tile_gateup(moe_ctx *ctx, const MxProduct &p, uint8_t *scales) {
-  pick<kGateUp, MOE_FP32>(ctx, p, scales);
+moe_status launch_mx_gateup(moe_ctx *ctx, const MxProduct &p, uint8_t *scales) {
+  launch<kGateUp, MOE_FP32>(ctx, p, scales);
   MOE_CHECK_LAUNCH("mx gate/up tile kernel");
   return MOE_OK;
 }
-moe_status launch_mx_tile_down(moe_ctx *ctx, int dtype, const MxProduct &p) {
+moe_status launch_mx_down(moe_ctx *ctx, int dtype, const MxProduct &p) {
   if (dtype == MOE_BF16)
-    pick<kDown, MOE_BF16>(ctx, p, nullptr);
+    launch<kDown, MOE_BF16>(ctx, p, nullptr);
   else
-    pick<kDown, MOE_FP32>(ctx, p, nullptr);
+    launch<kDown, MOE_FP32>(ctx, p, nullptr);
   MOE_CHECK_LAUNCH("mx down tile kernel");
   return MOE_OK;
 }

@@ -149,7 +149,8 @@ def product(moe, ctx, x, w, dtype):
 
 SIZES = [(1, 1, 32), (1, 16, 64), (2, 17, 96), (15, 33, 128), (16, 64, 160), (17, 100, 256), (31, 5, 288), (33, 257, 512),
          (64, 130, 544), (65, 256, 1024), (100, 300, 1536), (129, 513, 416), (257, 255, 768), (300, 1000, 2048),
-         (1, 4097, 6144), (3, 640, 16384), (40, 96, 6176), (513, 770, 288)]
+         (1, 4097, 6144), (3, 640, 16384), (40, 96, 6176), (513, 770, 288), (24, 129, 2560), (60, 200, 4096), (20, 2000, 512),
+         (31, 700, 1504), (257, 300, 4096)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -217,7 +218,7 @@ COUNTS = [[1], [0, 5, 0, 0, 17, 1], [0, 0], [16, 16, 0, 32], [3] * 70, [200, 0, 
 
 
 @pytest.mark.parametrize("i", range(len(COUNTS)))
-@pytest.mark.parametrize("N,K", [(96, 128), (130, 352)])
+@pytest.mark.parametrize("N,K", [(96, 128), (130, 352), (200, 1536), (257, 512)])
 def test_grouped(moe, ctx, i, N, K):
     counts = COUNTS[i]
     rng = np.random.default_rng(i)
@@ -346,7 +347,9 @@ def check_ffn(out, x, idx, w, experts, E, shared):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T,k,E,H,I,shared", [(1, 2, 8, 128, 64, True), (1, 8, 64, 320, 192, False), (2, 1, 1, 64, 64, True),
                                               (3, 4, 16, 192, 448, True), (33, 2, 5, 256, 128, True),
-                                              (70, 3, 9, 448, 320, False), (300, 2, 4, 128, 576, True)])
+                                              (70, 3, 9, 448, 320, False), (300, 2, 4, 128, 576, True),
+                                              (6, 2, 7, 512, 1024, True), (130, 2, 3, 1536, 512, True),
+                                              (700, 2, 3, 512, 512, False), (900, 1, 2, 192, 320, True)])
 def test_ffn(moe, ctx, dtype, T, k, E, H, I, shared):
     rng = np.random.default_rng(T + k + E)
     experts = Experts(moe, ctx, T, E + int(shared), H, I)

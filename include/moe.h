@@ -589,7 +589,9 @@ moe_status moe_latent_prompt(moe_ctx *ctx, const moe_latent_cfg *cfg, const moe_
  * at most 65536) is K / 2 bytes of codes and K / 32 scale bytes:
  *   codes [rows][K / 2]: element 2i in the low half of byte i. A code is a sign
  *     (bit 3) and 0, 0.5, 1, 1.5, 2, 3, 4 or 6 (bits 0 to 2).
- *   scales [rows][K / 32]: byte s stands for 2^(s - 127), 255 for NaN.
+ *   scales [rows][K / 32]: byte s stands for 2^(s - 127), 255 for NaN. Unlike
+ *     other pointers these need no alignment (products with K a multiple of 512
+ *     are faster with 16-byte aligned ones).
  * An element is its code's value times its block's scale. Types of unquantised
  * arrays: MOE_BF16, MOE_FP16 or MOE_FP32.
  *

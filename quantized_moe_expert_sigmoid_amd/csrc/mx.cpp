@@ -62,15 +62,15 @@ static moe_status product_check(const char *fn, moe_ctx *ctx, int dtype, const M
           "%s: %lld lines, %lld rows of x, %lld of out", fn, (long long)p.L, (long long)p.X, (long long)p.R);
   if (p.L == 0 || p.N == 0) return MOE_OK;
   REQUIRE(p.x && p.sx && p.w && p.sw && p.out, "%s: NULL pointer", fn);
-  REQUIRE(moe_aligned16(p.x) && moe_aligned16(p.w) && moe_aligned16(p.sx) && moe_aligned16(p.sw) && moe_aligned16(p.out),
-          "%s: x, w, their scales and out must be 16-byte aligned", fn);
+  REQUIRE(moe_aligned16(p.x) && moe_aligned16(p.w) && moe_aligned16(p.out),
+          "%s: the codes of x and w, and out, must be 16-byte aligned", fn);
   return MOE_OK;
 }
 
 // The product by the kernels that its lines call for.
 static moe_status product_run(moe_ctx *ctx, int dtype, MxProduct &p) {
   p.err = ctx->dev_small;
-  return mx_tiles(p.L, p.E) ? launch_mx_tile_product(ctx, dtype, p) : launch_mx_product(ctx, dtype, p);
+  return mx_tiles(ctx, p) ? launch_mx_tile_product(ctx, dtype, p) : launch_mx_product(ctx, dtype, p);
 }
 
 extern "C" moe_status moe_mx_matmul(moe_ctx *ctx, int dtype, const uint8_t *x, const uint8_t *sx, int64_t M,

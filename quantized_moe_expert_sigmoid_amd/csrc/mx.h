@@ -35,8 +35,8 @@ moe_status launch_mx_quantize(moe_ctx *ctx, int dtype, const void *x, int64_t ro
                               uint8_t *codes, uint8_t *scales);
 moe_status launch_mx_dequantize(moe_ctx *ctx, int dtype, const uint8_t *codes, const uint8_t *scales, int64_t rows,
                                 int K, void *out);
-// Whether a product of this many lines over E experts goes to the tile kernels.
-bool mx_tiles(int64_t lines, int E);
+// Whether a product goes to the tile kernels.
+bool mx_tiles(const moe_ctx *ctx, const MxProduct &p);
 // out = x w^T line by line
 moe_status launch_mx_product(moe_ctx *ctx, int dtype, const MxProduct &p);
 moe_status launch_mx_tile_product(moe_ctx *ctx, int dtype, const MxProduct &p);

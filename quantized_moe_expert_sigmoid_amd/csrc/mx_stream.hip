@@ -121,7 +121,7 @@ void pick(moe_ctx *ctx, const MxProduct &p) {
 
 template <int DTYPE>
 void launch(moe_ctx *ctx, const MxProduct &p) {
-  if (p.K % (4 * kMxBlock) == 0)
+  if (p.K % (4 * kMxBlock) == 0 && (((uintptr_t)p.sx | (uintptr_t)p.sw) & 3) == 0)
     pick<true, DTYPE>(ctx, p);
   else
     pick<false, DTYPE>(ctx, p);

@@ -17,6 +17,8 @@
 // A wave has the operands of the next product step in registers before the
 // present one begins, and a stage's place is loaded again while its last products
 // run: STAGES - 1 stages are in flight.
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "mx.h"
@@ -116,7 +118,7 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
     w[0] = p.table[u.e].gate, w[1] = p.table[u.e].up;
     sw[0] = p.table[u.e].s_gate, sw[1] = p.table[u.e].s_up;
   }
-  const int blocks = p.K / kMxBlock, steps = (blocks + KU - 1) / KU, full = blocks / KU;
+  const int blocks = p.K / kMxBlock, steps = (blocks + KU - 1) / KU;
   // sources: row r of the tile, the lines first, then the weights' rows (gate's, then up's)
   auto row_of = [&](int r, int &which) -> int64_t {
     if (r < BM) return max(mx_in_row(p, u.first + min(r, u.n - 1)), (int64_t)0);
@@ -140,26 +142,42 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
     const int64_t row = row_of(r, which);
     src_s[i] = (r < BM ? p.sx : sw[which]) + row * blocks + (WIDE ? 0 : lane % KU);
   }
-  auto load = [&](int s) {
-    const uint32_t to = lds0 + s % STAGES * kStage + wave * 1024, to_s = lds0 + kAt + s / kChunk % kChunks * kScales;
-    const int on = mx_uniform(s < steps ? -1 : 0), on_s = s % kChunk ? 0 : on;
-    // behind a row's end zeros
-    const bool there = s < full || KU * s + mine < blocks, there_s = s < full || KU * s + lane % KU < blocks;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      lds_load16(there ? src[i] + s * kRowB : mx_zeros, mx_uniform((int)(to + i * kWaves * 1024)), on);
-#pragma unroll
-    for (int i = 0; i < kLoadsS; ++i) {
-      const int r = (i * kWaves + wave) * kRowsS;
-      const uint32_t to_r = mx_uniform((int)(to_s + min(r, kRows - kRowsS) * (kScales / kRows)));
+  // piece i of stage s: rows of codes, then of scales. Sources go on by a stage each time they are used; those of the
+  // last stage, if it is not whole, are zeros where a row ends.
+  auto load = [&](int s, int i) {
+    const int on = mx_uniform(s < steps ? -1 : 0);
+    if (i < kLoads) {
+      lds_load16(src[i], mx_uniform((int)(lds0 + s % STAGES * kStage + (i * kWaves + wave) * 1024)), on);
+      src[i] += kRowB;
+    } else {
+      const int j = i - kLoads, r = (j * kWaves + wave) * kRowsS;
+      const int to = mx_uniform((int)(lds0 + kAt + s / kChunk % kChunks * kScales + min(r, kRows - kRowsS) * (kScales / kRows)));
+      const int on_s = mx_uniform(r < kRows && s % kChunk == 0 ? on : 0);
       if constexpr (WIDE)
-        lds_load16(src_s[i] + s * KU, to_r, mx_uniform(r < kRows ? on_s : 0));
+        lds_load16(src_s[j], to, on_s);
       else
-        lds_load1(there_s ? src_s[i] + s * KU : mx_zeros, to_r, mx_uniform(r < kRows ? on_s : 0));
+        lds_load1(src_s[j], to, on_s);
+      src_s[j] += KU;
     }
   };
+  auto last = [&](int s) {  // before the first piece of stage s
+    if (WIDE || s != blocks / KU || blocks % KU == 0) return;
+    if (KU * s + mine >= blocks)
 #pragma unroll
-  for (int s = 0; s < STAGES; ++s) load(s);
+      for (int i = 0; i < kLoads; ++i) src[i] = mx_zeros;
+    if (KU * s + lane % KU >= blocks)
+#pragma unroll
+      for (int i = 0; i < kLoadsS; ++i) src_s[i] = mx_zeros;
+  };
+  // A stage's pieces are spread over the products of kPhases product steps, from the one on in which its place is free.
+  constexpr int kSteps = KU / 2, kPhases = STAGES == 2 ? 2 : kSteps;
+  constexpr auto first_of = [](int phase) { return phase >= kPhases ? kPer : phase * kPer / kPhases; };
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) {
+    last(s);
+#pragma unroll
+    for (int i = 0; i < (s < STAGES - 1 ? kPer : first_of(1)); ++i) load(s, i);
+  }
 
   f32x16 acc[FN][FM];
 #pragma unroll
@@ -182,12 +200,12 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
   typedef int Words __attribute__((ext_vector_type(KU / 2)));
   typedef typename std::conditional<!WIDE, Words, typename std::conditional<KU == 8, int, uint16_t>::type>::type Scale;
   Scale xs[2][FM], ws[2][FN];
-  auto read = [&](int s, int k) {  // operands of product step k of stage s
+  auto read = [&](int s, int k, int i) {  // operand i of product step k of stage s
     const uint8_t *b = lds + s % STAGES * kStage + off[k];
-#pragma unroll
-    for (int i = 0; i < FN; ++i) wf[k & 1][i] = *reinterpret_cast<const i32x4 *>(b + row_w[i] * kRowB);
-#pragma unroll
-    for (int j = 0; j < FM; ++j) xf[k & 1][j] = *reinterpret_cast<const i32x4 *>(b + row_x[j] * kRowB);
+    if (i < FN)
+      wf[k & 1][i] = *reinterpret_cast<const i32x4 *>(b + row_w[i] * kRowB);
+    else
+      xf[k & 1][i - FN] = *reinterpret_cast<const i32x4 *>(b + row_x[i - FN] * kRowB);
   };
   auto read_scales = [&](int s, int to) {
     constexpr int kRowS = kScales / kRows;
@@ -198,34 +216,39 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
 #pragma unroll
     for (int j = 0; j < FM; ++j) xs[to][j] = *reinterpret_cast<const Scale *>(b + row_x[j] * kRowS);
   };
-  WAIT_VM((STAGES - 1) * kPer);
+  WAIT_VM((STAGES - 2) * kPer + first_of(1));
   asm volatile("s_barrier" ::: "memory");
-  read(0, 0);
+#pragma unroll
+  for (int i = 0; i < FN + FM; ++i) read(0, 0, i);
   read_scales(0, 0);
   auto stage = [&](int s, auto parity) {
     constexpr int P = decltype(parity)::value;
-    static_for<0, KU / 2>([&](auto kc) {
-      constexpr int k = decltype(kc)::value;
-      if constexpr (k + 1 < KU / 2) {
-        read(s, k + 1);
-      } else {  // this stage is read, the next one is there, for every wave
+    static_for<0, kSteps>([&](auto kc) {
+      constexpr int k = decltype(kc)::value, kPhase = (k + 1) % kSteps;
+      const int s_load = s + STAGES - (kPhase ? 1 : 0);
+      if constexpr (kPhase == 0) {  // this stage is read, the next one is there, for every wave
         WAIT_VM((STAGES - 2) * kPer);
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        read(s + 1, 0);
-        read_scales(s + 1, 1 - P);
-        load(s + STAGES);
+        last(s_load);
       }
       __builtin_amdgcn_sched_barrier(0);
+      // Between the products: the next step's operands, in the first half of them, and the loads.
+      constexpr int F = FN * FM, kHalf = F > 1 ? F / 2 : 1, R = FN + FM, kBegin = first_of(kPhase), kNum = first_of(kPhase + 1) - kBegin;
+      static_for<0, F>([&](auto tc) {
+        constexpr int t = decltype(tc)::value, i = t / FM, j = t % FM;
+        if constexpr (WIDE)
+          acc[i][j] = mfma32<k>(wf[k & 1][i], ws[P][i], xf[k & 1][j], xs[P][j], acc[i][j]);
+        else
+          acc[i][j] = mfma32<0>(wf[k & 1][i], ws[P][i][k], xf[k & 1][j], xs[P][j][k], acc[i][j]);
+        if constexpr (t < kHalf) {
 #pragma unroll
-      for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int j = 0; j < FM; ++j) {
-          if constexpr (WIDE)
-            acc[i][j] = mfma32<k>(wf[k & 1][i], ws[P][i], xf[k & 1][j], xs[P][j], acc[i][j]);
-          else
-            acc[i][j] = mfma32<0>(wf[k & 1][i], ws[P][i][k], xf[k & 1][j], xs[P][j][k], acc[i][j]);
+          for (int r = t * R / kHalf; r < (t + 1) * R / kHalf; ++r) read(kPhase ? s : s + 1, kPhase, r);
+          if constexpr (kPhase == 0 && t == kHalf - 1) read_scales(s + 1, 1 - P);
         }
-      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int l = kBegin + t * kNum / F; l < kBegin + (t + 1) * kNum / F; ++l) load(s_load, l);
+        __builtin_amdgcn_sched_barrier(0);
+      });
     });
   };
   for (int s = 0; s < steps; s += 2) {
@@ -341,38 +364,84 @@ void run(moe_ctx *ctx, const MxProduct &p, uint8_t *a_scales) {
                m, a_scales);
 }
 
-#ifndef T1
-#define T1 32
-#define T2 128
-#endif
-// Stages: as many as the LDS holds (a byte's word beside the codes: fewer).
+// The tiles there are, lines x rows of weights (gate/up: half as many of each). For a step of 256 k a workgroup takes
+// `full` us where every CU has its `per_cu` workgroups and `alone` us where a CU has one, most of it latency (measured
+// with 24576, 8192, 6144 and 4096 rows of 2048 to 8192 k; the estimates below are within 30% where the weights' bytes
+// are not the bound and put the tiles in the measured order but for differences of 10%). Few lines an expert want few
+// lines a tile (256 experts, 16384 lines of 6144 by 4096: 32 x 128 1074 us, 64 x 128 844, 128 x 128 862, 128 x 256 809,
+// 256 x 256 1043), a full chip large ones (4096 lines of 6144 by 24576: 817, 549, 419, 407, 376 us), little work many.
+struct Tile {
+  int bm, bn, per_cu;
+  double full, alone;
+};
+constexpr Tile kTiles[] = {{32, 128, 2, 0.68, 0.36}, {64, 128, 2, 0.95, 0.51}, {128, 128, 2, 1.45, 0.9},
+                           {128, 256, 1, 1.41, 1.2}, {256, 256, 1, 2.6, 2.2}};
+
+double tile_time(const moe_ctx *ctx, const MxProduct &p, const Tile &t, int cols) {
+  // experts with lines have their share of them and half a tile more, but at least one tile
+  const double active = p.offsets ? (double)(p.L < p.E ? p.L : p.E) : 1;
+  double units = p.offsets ? active * std::max(1.0, (double)p.L / (active * t.bm) + 0.5) : (double)((p.L + t.bm - 1) / t.bm);
+  units += (double)((p.shared + t.bm - 1) / t.bm);
+  const double wg = units * ((p.N + cols - 1) / cols), slots = (double)t.per_cu * ctx->n_cu;
+  const double rounds = std::floor(wg / slots), rest = wg - rounds * slots;
+  return (p.K + 255) / 256 * (rounds * t.full + (rest < 1 ? 0.0 : rest <= ctx->n_cu ? t.alone : t.full)) + 5;
+}
+
+int pick(const moe_ctx *ctx, const MxProduct &p, int mode, double *time) {
+  int best = 0;
+  double least = 1e30;
+  for (int i = 0; i < (int)(sizeof kTiles / sizeof *kTiles); ++i) {
+    const double v = tile_time(ctx, p, kTiles[i], kTiles[i].bn / (mode == kGateUp ? 2 : 1));
+    if (v < least) least = v, best = i;
+  }
+  if (time) *time = least;
+  return best;
+}
+
+// Stages: as many as the LDS holds for `per_cu` workgroups a CU (scales as words: fewer).
 template <bool WIDE, int MODE, int DTYPE>
-void pick(moe_ctx *ctx, const MxProduct &p, uint8_t *a_scales) {
-  const int64_t lines = p.offsets ? p.L / p.E : p.L;
-  if (lines > T2)
-    run<256, 256, 2, 4, 4, 4, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales);
-  else if (lines > T1)
-    run<128, 256, 2, 4, 8, WIDE ? 3 : 2, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales);
-  else
-    run<32, 128, 1, 4, 8, 3, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales);
+void launch_tile(moe_ctx *ctx, const MxProduct &p, uint8_t *a_scales) {
+#ifdef FORCE_TILE
+  switch (FORCE_TILE) {
+#else
+  switch (pick(ctx, p, MODE, nullptr)) {
+#endif
+    case 0: run<32, 128, 1, 4, 8, 3, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales); break;
+    case 1: run<64, 128, 2, 2, 8, WIDE ? 3 : 2, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales); break;
+    case 2: run<128, 128, 2, 2, WIDE ? 8 : 4, WIDE ? 2 : 3, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales); break;
+    case 3: run<128, 256, 2, 4, 8, WIDE ? 3 : 2, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales); break;
+    default: run<256, 256, 2, 4, 4, 4, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales); break;
+  }
 }
 template <int MODE, int DTYPE>
 void launch(moe_ctx *ctx, const MxProduct &p, uint8_t *a_scales) {
-  if (p.K % (16 * kMxBlock) == 0)
-    pick<true, MODE, DTYPE>(ctx, p, a_scales);
+  if (p.K % (16 * kMxBlock) == 0 && moe_aligned16(p.sx) && moe_aligned16(p.sw))  // sw: NULL with a table, whose own are aligned
+    launch_tile<true, MODE, DTYPE>(ctx, p, a_scales);
   else
-    pick<false, MODE, DTYPE>(ctx, p, a_scales);
+    launch_tile<false, MODE, DTYPE>(ctx, p, a_scales);
 }
 
 }  // namespace
 
-#ifdef FORCE_STREAM
-bool mx_tiles(int64_t, int) { return false; }
-#elif defined(FORCE_TILE)
-bool mx_tiles(int64_t, int) { return true; }
-#else
-bool mx_tiles(int64_t lines, int E) { return E > 1 || lines > 16; }
+// Up to 64 lines an expert can go to the kernels without tiles (mx_stream.hip), whose time the requests of all
+// workgroups' rows make: with 16 NM lines and s steps of 1024 k each wave, 1 + NM (less: the lines there are) times
+// s + 8, 0.1225 us for every 256 workgroups. 4096 rows of 6144: 1, 16, 32 and 64 lines 4.9, 5.9, 7.6 and 11.1 us there,
+// 13.2 us in tiles of 32 x 128; 6144 rows of 2048: 5.0, 6.5, 8.3 and 12.1, 7.6 us in tiles. Where bytes are the bound,
+// tiles read them at 5 TB/s, the others for one line alone (24576 rows of 6144: 17 us, tiles 20.5; 8 lines 22.9 and
+// 20.9) and at about 3.5 for more or for several experts (4 tokens of 8 experts, 4096 rows of 6144: 104 and 73 us).
+bool mx_tiles(const moe_ctx *ctx, const MxProduct &p) {
+#ifdef FORCE_TILE
+  return true;
 #endif
+  const double active = p.offsets ? (double)(p.L < p.E ? p.L : p.E) : 1, lines = (double)p.L / active;
+  if (lines > 64) return true;
+  const double nm = lines <= 16 ? lines / 16 : lines <= 32 ? 2 : 4, wg = active * ((p.N + 15) / 16) / ctx->n_cu;
+  const double stream = 2.5 + (wg < 1 ? 1 : wg) * (1 + nm) * 0.1225 * ((p.K + 1023) / 1024 + 8);
+  const double bytes = active * p.N * (double)p.K * 17 / 32 * 1e-6;  // over TB/s: us
+  double tile;
+  pick(ctx, p, kPlain, &tile);
+  return std::max(stream, bytes / (p.L == 1 ? 5 : 3.5) + 2.5) > std::max(tile, bytes / 5 + 3.5);
+}
 
 moe_status launch_mx_tile_product(moe_ctx *ctx, int dtype, const MxProduct &p) {
   switch (dtype) {

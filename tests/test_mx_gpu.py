@@ -183,6 +183,21 @@ def test_product_small_and_large_scales(moe, ctx):
         ref.check_product(product(moe, ctx, x, w, FP32), ref.dequantize(*x), ref.dequantize(*w), (lo, wlo))
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 64, 512), (40, 200, 512), (200, 300, 1024), (300, 300, 128)])
+def test_product_unaligned_scales(moe, ctx, M, N, K):
+    """Scales at any address (a matrix of a stack, for instance)."""
+    rng = np.random.default_rng(K)
+    x, w = ref.random_matrix(rng, M, K), ref.random_matrix(rng, N, K)
+    for ax, aw in ((1, 0), (0, 3), (4, 8)):
+        sx = torch.empty(ax + x[1].size, dtype=torch.uint8, device="cuda")[ax:].view(M, -1)
+        sw = torch.empty(aw + w[1].size, dtype=torch.uint8, device="cuda")[aw:].view(N, -1)
+        sx.copy_(torch.from_numpy(x[1]))
+        sw.copy_(torch.from_numpy(w[1]))
+        out = torch.empty((M, N), device="cuda")
+        moe.moe_mx_matmul(ctx, torch.from_numpy(x[0]).cuda(), sx, torch.from_numpy(w[0]).cuda(), sw, out)
+        ref.check_product(out, ref.dequantize(*x), ref.dequantize(*w), (M, ax, aw))
+
+
 def test_product_nothing(moe, ctx):
     e = lambda *s: torch.empty(s, dtype=torch.uint8, device="cuda")  # noqa: E731
     out = torch.full((0, 8), 1.0, device="cuda")

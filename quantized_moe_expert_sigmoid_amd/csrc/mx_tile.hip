@@ -64,15 +64,17 @@ __device__ __forceinline__ f32x16 mfma32(i32x4 a, int sa, i32x4 b, int sb, f32x1
 
 enum { kPlain, kDown, kGateUp };
 
-// How workgroups map to tiles: blocks of G units x GN column tiles go round the 8 XCDs; within one, units run fastest.
+// How workgroups map to tiles: blocks of g units x gn column tiles go round the 8 XCDs; within one, units run fastest.
+// With a unit an expert nothing is shared but a few lines, and single tiles go round, so that all XCDs have as many (one
+// token of 9 experts: one XCD had 72 workgroups and another 40).
 struct TileMap {
   int n_tiles, units, g, gn;
 };
-TileMap tile_map(int64_t units, int n_tiles) {
+TileMap tile_map(int64_t units, int n_tiles, bool apart) {
   TileMap m;
   m.n_tiles = n_tiles, m.units = (int)units;
-  m.g = units < 4 ? (int)units : 4;
-  m.gn = 32 / m.g < n_tiles ? 32 / m.g : n_tiles;
+  m.g = apart ? 1 : units < 4 ? (int)units : 4;
+  m.gn = apart ? 1 : 32 / m.g < n_tiles ? 32 / m.g : n_tiles;
   return m;
 }
 unsigned tile_grid(const TileMap &m) {
@@ -119,28 +121,26 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
     sw[0] = p.table[u.e].s_gate, sw[1] = p.table[u.e].s_up;
   }
   const int blocks = p.K / kMxBlock, steps = (blocks + KU - 1) / KU;
-  // sources: row r of the tile, the lines first, then the weights' rows (gate's, then up's)
-  auto row_of = [&](int r, int &which) -> int64_t {
-    if (r < BM) return max(mx_in_row(p, u.first + min(r, u.n - 1)), (int64_t)0);
-    const int n = r - BM;
-    which = MODE == kGateUp && n >= kCols;
-    return min(n0 + n - which * kCols, p.N - 1);
-  };
+  // sources: the lines first, then the weights' rows (gate's, then up's). What a load instruction of codes has is known
+  // here, where all waves' rows of it are of one kind; deciding lane by lane cost 4 us of a workgroup's start.
+  auto x_row = [&](int r) { return max(mx_in_row(p, u.first + min(r, u.n - 1)), (int64_t)0) * blocks; };
+  auto w_row = [&](int n) { return (int64_t)min(n0 + n, p.N - 1) * blocks; };
   const int mine = (lane % KU) ^ swz((wave * kRowsL + lane / KU) & 15);  // the unit of its row that a lane loads
   const uint8_t *src[kLoads], *src_s[kLoadsS];
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int r = (i * kWaves + wave) * kRowsL + lane / KU;
-    int which = 0;
-    const int64_t row = row_of(r, which);
-    src[i] = (r < BM ? p.x : w[which]) + (row * blocks + mine) * 16;
-  }
+  static_for<0, kLoads>([&](auto ic) {
+    constexpr int first = decltype(ic)::value * kWaves * kRowsL, n = first - BM;
+    static_assert(BM % (kWaves * kRowsL) == 0 && kCols % (kWaves * kRowsL) == 0);
+    const int r = wave * kRowsL + lane / KU;
+    if constexpr (n < 0)
+      src[ic] = p.x + (x_row(first + r) + mine) * 16;
+    else
+      src[ic] = w[n >= kCols] + (w_row(n % kCols + r) + mine) * 16;
+  });
 #pragma unroll
   for (int i = 0; i < kLoadsS; ++i) {
-    const int r = min((i * kWaves + wave) * kRowsS, kRows - kRowsS) + (WIDE ? lane : lane / KU);
-    int which = 0;
-    const int64_t row = row_of(r, which);
-    src_s[i] = (r < BM ? p.sx : sw[which]) + row * blocks + (WIDE ? 0 : lane % KU);
+    const int r = min((i * kWaves + wave) * kRowsS, kRows - kRowsS) + (WIDE ? lane : lane / KU), n = r - BM;
+    const int64_t at = n < 0 ? x_row(r) : w_row(MODE == kGateUp && n >= kCols ? n - kCols : n);
+    src_s[i] = (n < 0 ? p.sx : sw[MODE == kGateUp && n >= kCols]) + at + (WIDE ? 0 : lane % KU);
   }
   // piece i of stage s: rows of codes, then of scales. Sources go on by a stage each time they are used; those of the
   // last stage, if it is not whole, are zeros where a row ends.
@@ -294,7 +294,7 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
         uint32_t top = 0;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          a[e] = moe_silu_f32(acc[i][j][e]) * up[i][j][e];
+          a[e] = mx_silu(acc[i][j][e]) * up[i][j][e];
           top = max(top, __float_as_uint(a[e]) & 0x7fffffffu);
         }
         // the other half of the wave has the block's other 16 values
@@ -355,7 +355,7 @@ template <int BM, int BN, int WM, int WN, int KU, int STAGES, int OCC, bool WIDE
 void run(moe_ctx *ctx, const MxProduct &p, uint8_t *a_scales) {
   const int64_t units = (p.offsets ? (p.L < p.E ? p.L : p.L / BM + p.E) : (p.L + BM - 1) / BM) + (p.shared + BM - 1) / BM;
   const int cols = MODE == kGateUp ? BN / 2 : BN;
-  const TileMap m = tile_map(units, (p.N + cols - 1) / cols);
+  const TileMap m = tile_map(units, (p.N + cols - 1) / cols, p.offsets && p.L <= (int64_t)p.E * BM);
   auto kernel = mx_tile_kernel<BM, BN, WM, WN, KU, STAGES, OCC, WIDE, MODE, DTYPE>;
   if (MODE == kPlain)
     hipLaunchKernelGGL(kernel, dim3(tile_grid(m)), dim3(WM * WN * 64), 0, ctx->stream, p, m, a_scales);
@@ -365,7 +365,7 @@ void run(moe_ctx *ctx, const MxProduct &p, uint8_t *a_scales) {
 }
 
 // The tiles there are, lines x rows of weights (gate/up: half as many of each). For a step of 256 k a workgroup takes
-// `full` us where every CU has its `per_cu` workgroups and `alone` us where a CU has one, most of it latency (measured
+// `full` us where every CU has its `per_cu` workgroups, less with fewer, and `alone` us where a CU has one (measured
 // with 24576, 8192, 6144 and 4096 rows of 2048 to 8192 k; the estimates below are within 30% where the weights' bytes
 // are not the bound and put the tiles in the measured order but for differences of 10%). Few lines an expert want few
 // lines a tile (256 experts, 16384 lines of 6144 by 4096: 32 x 128 1074 us, 64 x 128 844, 128 x 128 862, 128 x 256 809,
@@ -374,7 +374,7 @@ struct Tile {
   int bm, bn, per_cu;
   double full, alone;
 };
-constexpr Tile kTiles[] = {{32, 128, 2, 0.68, 0.36}, {64, 128, 2, 0.95, 0.51}, {128, 128, 2, 1.45, 0.9},
+constexpr Tile kTiles[] = {{32, 64, 4, 0.84, 0.27}, {32, 128, 2, 0.68, 0.36}, {64, 128, 2, 0.95, 0.51}, {128, 128, 2, 1.45, 0.9},
                            {128, 256, 1, 1.41, 1.2}, {256, 256, 1, 2.6, 2.2}};
 
 double tile_time(const moe_ctx *ctx, const MxProduct &p, const Tile &t, int cols) {
@@ -383,8 +383,8 @@ double tile_time(const moe_ctx *ctx, const MxProduct &p, const Tile &t, int cols
   double units = p.offsets ? active * std::max(1.0, (double)p.L / (active * t.bm) + 0.5) : (double)((p.L + t.bm - 1) / t.bm);
   units += (double)((p.shared + t.bm - 1) / t.bm);
   const double wg = units * ((p.N + cols - 1) / cols), slots = (double)t.per_cu * ctx->n_cu;
-  const double rounds = std::floor(wg / slots), rest = wg - rounds * slots;
-  return (p.K + 255) / 256 * (rounds * t.full + (rest < 1 ? 0.0 : rest <= ctx->n_cu ? t.alone : t.full)) + 5;
+  const double rounds = std::floor(wg / slots), rest = std::ceil((wg - rounds * slots) / ctx->n_cu);
+  return (p.K + 255) / 256 * (rounds * t.full + (rest == 0 ? 0.0 : std::max(t.alone, rest * t.full / t.per_cu))) + 5;
 }
 
 int pick(const moe_ctx *ctx, const MxProduct &p, int mode, double *time) {
@@ -406,10 +406,11 @@ void launch_tile(moe_ctx *ctx, const MxProduct &p, uint8_t *a_scales) {
 #else
   switch (pick(ctx, p, MODE, nullptr)) {
 #endif
-    case 0: run<32, 128, 1, 4, 8, 3, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales); break;
-    case 1: run<64, 128, 2, 2, 8, WIDE ? 3 : 2, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales); break;
-    case 2: run<128, 128, 2, 2, WIDE ? 8 : 4, WIDE ? 2 : 3, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales); break;
-    case 3: run<128, 256, 2, 4, 8, WIDE ? 3 : 2, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales); break;
+    case 0: run<32, 64, 1, 2, 8, 3, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales); break;
+    case 1: run<32, 128, 1, 4, 8, 3, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales); break;
+    case 2: run<64, 128, 2, 2, 8, WIDE ? 3 : 2, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales); break;
+    case 3: run<128, 128, 2, 2, WIDE ? 8 : 4, WIDE ? 2 : 3, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales); break;
+    case 4: run<128, 256, 2, 4, 8, WIDE ? 3 : 2, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales); break;
     default: run<256, 256, 2, 4, 4, 4, 2, WIDE, MODE, DTYPE>(ctx, p, a_scales); break;
   }
 }

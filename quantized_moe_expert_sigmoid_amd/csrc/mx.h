@@ -19,13 +19,17 @@ struct MxProduct {
   int64_t w_e, sw_e;
   const moe_mx_expert_w *table;
   int N, K;
-  // lines: line l is row in_rows[l] / k of x (NULL: l) and goes to row out_rows[l] of out (NULL: l)
+  // lines: line l is row in_rows[l] / k of x (NULL: l / k) and goes to row out_rows[l] of out (NULL: l)
   const int32_t *offsets;  // [E + 1], expert e's lines are offsets[e] ..; NULL: one expert has all L of them
+  const int32_t *ids;      // or line l is expert ids[l]'s, none's if that is no expert or one of token l / per_token's earlier lines
+  int per_token;
   int E;
   int64_t L;
   const int32_t *in_rows, *out_rows;
   int k;
-  int64_t shared;  // lines L .. L + shared - 1 are expert E's; with in_rows they are rows 0 .. of x, else rows L ..
+  int64_t shared;  // lines L .. L + shared - 1 are expert E's and rows 0 .. of x where `tokens`, else rows L ..
+  bool tokens;     // x has a row a token
+  int x_dtype;     // gate/up with ids: x is values of this type and sx unused
   void *out;
   int64_t R;  // rows of out
   uint32_t *err;
@@ -40,6 +44,9 @@ bool mx_tiles(const moe_ctx *ctx, const MxProduct &p);
 // out = x w^T line by line
 moe_status launch_mx_product(moe_ctx *ctx, int dtype, const MxProduct &p);
 moe_status launch_mx_tile_product(moe_ctx *ctx, int dtype, const MxProduct &p);
+// The same for one line a unit (ids): gate/up's x is then values, quantised by every workgroup for itself.
+moe_status launch_mx_gateup_one(moe_ctx *ctx, const MxProduct &p, uint8_t *scales);
+moe_status launch_mx_down_one(moe_ctx *ctx, int dtype, const MxProduct &p);
 // silu(x gate^T) * (x up^T) line by line (the table's gate and up), in 4 bits: out's row l is line l
 moe_status launch_mx_gateup(moe_ctx *ctx, const MxProduct &p, uint8_t *scales);
 // the table's down
@@ -94,6 +101,41 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
 }
 // 2^(s - 127), s < 255
 __device__ __forceinline__ float mx_scale_value(uint32_t s) { return __uint_as_float(s ? s << 23 : 0x400000u); }
+
+template <int DTYPE>
+__device__ __forceinline__ void mx_load8(const void *p, float (&v)[8]) {
+  if constexpr (DTYPE == MOE_FP32) {
+    const f32x4 a = reinterpret_cast<const f32x4 *>(p)[0], b = reinterpret_cast<const f32x4 *>(p)[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+  } else {
+    const typename MxOut<DTYPE>::V a = reinterpret_cast<const typename MxOut<DTYPE>::V *>(p)[0],
+                                   b = reinterpret_cast<const typename MxOut<DTYPE>::V *>(p)[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (float)a[i], v[4 + i] = (float)b[i];
+  }
+}
+
+// Maximum over the four lanes of a quad, in all of them.
+__device__ __forceinline__ uint32_t mx_quad_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xb1, 0xf, 0xf, true));  // lanes 1, 0, 3, 2
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true));  // lanes 2, 3, 0, 1
+}
+
+// Codes of a thread's 8 values of a block and, in all four lanes, the block's scale byte.
+__device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], uint32_t &byte) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);  // orders NaN above infinity
+  byte = mx_scale_byte(mx_quad_max(top));
+  if (byte == 255) return 0;
+  const float s = mx_scale_value(byte);
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], s, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], s, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], s, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], s, 3);
+}
 
 // silu(g) = g / (1 + 2^(-g log2 e)) with the hardware's exponential and reciprocal, each within a unit in the last place;
 // the product with log2 e in two parts, since its rounding, times g, is an error of the exponential. Within 2^-21 of the
@@ -188,10 +230,25 @@ __device__ __forceinline__ MxUnit mx_unit(const MxProduct &p, int64_t u) {
   return r;
 }
 
+// Unit u where each line is one: p.ids' lines, then the shared expert's.
+__device__ __forceinline__ MxUnit mx_unit_one(const MxProduct &p, int u) {
+  if (u >= p.L) return MxUnit{p.E, u, u < p.L + p.shared ? 1 : 0};
+  const int id = p.ids[u];
+  bool ok = id >= 0 && id < p.E;
+  for (int i = u / p.per_token * p.per_token; i < u; ++i) ok &= p.ids[i] != id;
+  if (!ok && id != -1) atomicOr(p.err, (uint32_t)ERRF_BAD_INDEX);
+  return MxUnit{mx_uniform(id), u, mx_uniform(ok ? 1 : 0)};
+}
+
 // Row of x of a line, and where its result goes; -1: out of range, which is reported.
 __device__ __forceinline__ int64_t mx_in_row(const MxProduct &p, int64_t line) {
   int64_t r = line;
-  if (p.in_rows) r = line < p.L ? p.in_rows[line] / p.k : line - p.L;
+  if (p.tokens && line >= p.L)
+    r = line - p.L;
+  else if (p.in_rows)
+    r = p.in_rows[line] / p.k;
+  else if (p.tokens)
+    r = line / p.k;
   if (r >= 0 && r < p.X) return r;
   atomicOr(p.err, (uint32_t)ERRF_MX);
   return -1;

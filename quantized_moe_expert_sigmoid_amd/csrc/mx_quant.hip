@@ -13,41 +13,6 @@
 
 namespace {
 
-template <int DTYPE>
-__device__ __forceinline__ void load8(const void *p, float (&v)[8]) {
-  if constexpr (DTYPE == MOE_FP32) {
-    const f32x4 a = reinterpret_cast<const f32x4 *>(p)[0], b = reinterpret_cast<const f32x4 *>(p)[1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
-  } else {
-    const typename MxOut<DTYPE>::V a = reinterpret_cast<const typename MxOut<DTYPE>::V *>(p)[0],
-                                   b = reinterpret_cast<const typename MxOut<DTYPE>::V *>(p)[1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (float)a[i], v[4 + i] = (float)b[i];
-  }
-}
-
-// Maximum over the four lanes of a quad, in all of them.
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xb1, 0xf, 0xf, true));  // lanes 1, 0, 3, 2
-  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true));  // lanes 2, 3, 0, 1
-}
-
-// Codes of a thread's 8 values of a block and, in all four lanes, the block's scale byte.
-__device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t &byte) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);  // orders NaN above infinity
-  byte = mx_scale_byte(quad_max(top));
-  if (byte == 255) return 0;
-  const float s = mx_scale_value(byte);
-  uint32_t w = 0;
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], s, 0);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], s, 1);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], s, 2);
-  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], s, 3);
-}
-
 // n threads' worth of values, `segs` threads a row (a multiple of four), rows x_t elements apart.
 template <int DTYPE>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(const void *x, int64_t n, int segs, int64_t x_t,
@@ -57,9 +22,9 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const void *x, int64_t
   if (i >= n) return;  // whole quads: n is a multiple of four
   const int64_t row = i / segs;
   float v[8];
-  load8<DTYPE>(static_cast<const T *>(x) + row * x_t + (i - row * segs) * 8, v);
+  mx_load8<DTYPE>(static_cast<const T *>(x) + row * x_t + (i - row * segs) * 8, v);
   uint32_t byte;
-  codes[i] = codes8(v, byte);
+  codes[i] = mx_codes8(v, byte);
   if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
 }
 
@@ -112,25 +77,28 @@ __global__ __launch_bounds__(256) void mx_combine_kernel(const typename MxOut<Y>
   const int h = (int)(blockIdx.x % per * 256 + threadIdx.x) * 4;
   if (h >= H) return;
   bool used[kMaxK];
+  int id[kMaxK];
+  float f[kMaxK];
   V v[kMaxK], sh = {};
   if (has_shared) sh = *reinterpret_cast<const V *>(y + (T * (int64_t)k + t) * H + h);
 #pragma unroll
   for (int j = 0; j < kMaxK; ++j) {
-    used[j] = false;
-    if (j < k) {
-      const int id = idx[t * k + j];
-      used[j] = w[t * k + j] != 0.0f && id >= 0 && id < E;
-      for (int i = 0; i < j; ++i) used[j] &= idx[t * k + i] != id;
-      if (used[j]) v[j] = *reinterpret_cast<const V *>(y + (t * k + j) * H + h);
-    }
+    id[j] = idx[t * k + min(j, k - 1)];
+    f[j] = w[t * k + min(j, k - 1)];
+  }
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) {
+    used[j] = j < k && f[j] != 0.0f && id[j] >= 0 && id[j] < E;
+#pragma unroll
+    for (int i = 0; i < j; ++i) used[j] &= id[i] != id[j];
+    if (used[j]) v[j] = *reinterpret_cast<const V *>(y + (t * k + j) * H + h);
   }
   f32x4 acc = {(float)sh[0], (float)sh[1], (float)sh[2], (float)sh[3]};
 #pragma unroll
   for (int j = 0; j < kMaxK; ++j)
     if (used[j]) {
-      const float f = w[t * k + j];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(f, (float)v[j][c], acc[c]);
+      for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(f[j], (float)v[j][c], acc[c]);
     }
   *reinterpret_cast<typename MxOut<DTYPE>::V *>(out + t * H + h) = MxOut<DTYPE>::of(acc);
 }

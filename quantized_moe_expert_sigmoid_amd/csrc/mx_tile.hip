@@ -14,6 +14,10 @@
 // lane reads the word it needs and the instruction picks a byte. Other rows' scales
 // come a byte a lane, each into a word of its own.
 //
+// BM = 0 is for one line a unit: its codes lie in LDS from the start (for gate/up the
+// workgroup makes them from the values, while it waits for the expert's addresses),
+// all columns of a product are that line, and only weights come stage by stage.
+//
 // A wave has the operands of the next product step in registers before the
 // present one begins, and a stage's place is loaded again while its last products
 // run: STAGES - 1 stages are in flight.
@@ -64,6 +68,8 @@ __device__ __forceinline__ f32x16 mfma32(i32x4 a, int sa, i32x4 b, int sb, f32x1
 
 enum { kPlain, kDown, kGateUp };
 
+constexpr int kOneK = 8192;  // the longest row of one-line units
+
 // How workgroups map to tiles: blocks of g units x gn column tiles go round the 8 XCDs; within one, units run fastest.
 // With a unit an expert nothing is shared but a few lines, and single tiles go round, so that all XCDs have as many (one
 // token of 9 experts: one XCD had 72 workgroups and another 40).
@@ -85,7 +91,8 @@ unsigned tile_grid(const TileMap &m) {
 template <int BM, int BN, int WM, int WN, int KU, int STAGES, int OCC, bool WIDE, int MODE, int DTYPE>
 __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, TileMap map, uint8_t *a_scales) {
   typedef MxOut<DTYPE> O;
-  constexpr int kWaves = WM * WN, FM = BM / WM / 32, FN = BN / WN / 32;
+  constexpr bool kOne = BM == 0;
+  constexpr int kWaves = WM * WN, FM = kOne ? 1 : BM / WM / 32, FN = BN / WN / 32;
   constexpr int kRows = BM + BN, kRowB = KU * 16, kStage = kRows * kRowB, kAt = STAGES * kStage;
   // scales: stages of a load, loads kept, bytes of one
   constexpr int kChunk = WIDE ? 16 / KU : 1, kChunks = (STAGES + kChunk - 2) / kChunk + 1, kScales = kRows * (WIDE ? 16 : 4 * KU);
@@ -94,15 +101,71 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
   constexpr int kCols = MODE == kGateUp ? BN / 2 : BN;  // of the result
   static_assert(kRows % (kRowsL * kWaves) == 0 && kWaves * kRowsL % 16 == 0 && (KU == 4 || KU == 8));
   static_assert(MODE != kGateUp || FN % 2 == 0 || (FN == 1 && WN % 2 == 0));
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * kStage + kChunks * kScales];
+  // one line's codes and scales (in bytes, or words), and a stage more, which is read but not used
+  constexpr int kLine = kAt + kChunks * kScales, kLineS = kLine + kOneK / 2 + kRowB, kLineEnd = kLineS + (kOneK / 32 + KU) * (WIDE ? 1 : 4);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kOne ? kLineEnd : kLine];
 
   const int xcd = blockIdx.x & 7, j0 = blockIdx.x >> 3, per_block = map.g * map.gn;
   const int block = j0 / per_block * 8 + xcd, rest = j0 % per_block, across = (map.n_tiles + map.gn - 1) / map.gn;
   const int unit = block / across * map.g + rest % map.g, nt = block % across * map.gn + rest / map.g;
   if (unit >= map.units || nt >= map.n_tiles) return;
-  const MxUnit u = mx_unit<BM>(p, unit);
-  if (u.n == 0) return;
-  const int n0 = nt * kCols;
+  const int n0 = nt * kCols, blocks = p.K / kMxBlock, steps = (blocks + KU - 1) / KU;
+  MxUnit u;
+  if constexpr (kOne) {
+    constexpr int kChunk8 = kOneK / 8 / (kWaves * 64);  // words of eight codes a thread
+    const int64_t row = p.tokens ? (unit < p.L ? unit / p.k : unit - p.L) : unit;
+    uint32_t code[kChunk8], byte[kChunk8];
+    if constexpr (MODE == kGateUp) {
+      float v[kChunk8][8];
+      auto values = [&](auto type) {
+        typedef typename MxOut<decltype(type)::value>::T T;
+#pragma unroll
+        for (int i = 0; i < kChunk8; ++i) {
+          const int c = i * kWaves * 64 + threadIdx.x;
+          if (c < blocks * 4) mx_load8<decltype(type)::value>(reinterpret_cast<const T *>(p.x) + row * p.K + c * 8, v[i]);
+        }
+      };
+      if (p.x_dtype == MOE_FP32)
+        values(std::integral_constant<int, MOE_FP32>{});
+      else if (p.x_dtype == MOE_BF16)
+        values(std::integral_constant<int, MOE_BF16>{});
+      else
+        values(std::integral_constant<int, MOE_FP16>{});
+      u = mx_unit_one(p, unit);
+      if (u.n == 0) return;
+#pragma unroll
+      for (int i = 0; i < kChunk8; ++i)
+        if (i * kWaves * 64 + threadIdx.x < blocks * 4) code[i] = mx_codes8(v[i], byte[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kChunk8; ++i) {
+        const int c = i * kWaves * 64 + threadIdx.x;
+        if (c < blocks * 4) {
+          code[i] = reinterpret_cast<const uint32_t *>(p.x)[row * blocks * 4 + c];
+          byte[i] = p.sx[row * blocks + c / 4];
+        }
+      }
+      u = mx_unit_one(p, unit);
+      if (u.n == 0) return;
+    }
+#pragma unroll
+    for (int i = 0; i < kChunk8; ++i) {
+      const int c = i * kWaves * 64 + threadIdx.x;
+      if (c < steps * KU * 4) {  // zeros behind the row's end
+        reinterpret_cast<uint32_t *>(lds + kLine)[c] = c < blocks * 4 ? code[i] : 0;
+        const uint32_t s = c < blocks * 4 ? byte[i] : 0;
+        if ((c & 3) == 0) {
+          if constexpr (WIDE)
+            lds[kLineS + c / 4] = (uint8_t)s;
+          else
+            reinterpret_cast<uint32_t *>(lds + kLineS)[c / 4] = s;
+        }
+      }
+    }
+  } else {
+    u = mx_unit<BM>(p, unit);
+    if (u.n == 0) return;
+  }
   const int lane = threadIdx.x & 63, wave = mx_uniform((int)(threadIdx.x >> 6)), l32 = lane & 31, hl = lane >> 5;
   const int wm = wave % WM, wn = wave / WM;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
@@ -120,7 +183,6 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
     w[0] = p.table[u.e].gate, w[1] = p.table[u.e].up;
     sw[0] = p.table[u.e].s_gate, sw[1] = p.table[u.e].s_up;
   }
-  const int blocks = p.K / kMxBlock, steps = (blocks + KU - 1) / KU;
   // sources: the lines first, then the weights' rows (gate's, then up's). What a load instruction of codes has is known
   // here, where all waves' rows of it are of one kind; deciding lane by lane cost 4 us of a workgroup's start.
   auto x_row = [&](int r) { return max(mx_in_row(p, u.first + min(r, u.n - 1)), (int64_t)0) * blocks; };
@@ -129,7 +191,7 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
   const uint8_t *src[kLoads], *src_s[kLoadsS];
   static_for<0, kLoads>([&](auto ic) {
     constexpr int first = decltype(ic)::value * kWaves * kRowsL, n = first - BM;
-    static_assert(BM % (kWaves * kRowsL) == 0 && kCols % (kWaves * kRowsL) == 0);
+    static_assert((kOne || BM % (kWaves * kRowsL) == 0) && kCols % (kWaves * kRowsL) == 0);
     const int r = wave * kRowsL + lane / KU;
     if constexpr (n < 0)
       src[ic] = p.x + (x_row(first + r) + mine) * 16;
@@ -204,6 +266,8 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
     const uint8_t *b = lds + s % STAGES * kStage + off[k];
     if (i < FN)
       wf[k & 1][i] = *reinterpret_cast<const i32x4 *>(b + row_w[i] * kRowB);
+    else if (kOne)
+      xf[k & 1][0] = *reinterpret_cast<const i32x4 *>(lds + kLine + s * kRowB + (KU / 2 * hl + k) * 16);
     else
       xf[k & 1][i - FN] = *reinterpret_cast<const i32x4 *>(b + row_x[i - FN] * kRowB);
   };
@@ -214,10 +278,11 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
 #pragma unroll
     for (int i = 0; i < FN; ++i) ws[to][i] = *reinterpret_cast<const Scale *>(b + row_w[i] * kRowS);
 #pragma unroll
-    for (int j = 0; j < FM; ++j) xs[to][j] = *reinterpret_cast<const Scale *>(b + row_x[j] * kRowS);
+    for (int j = 0; j < FM; ++j)
+      xs[to][j] = *reinterpret_cast<const Scale *>(kOne ? lds + kLineS + (s * KU + KU / 2 * hl) * (WIDE ? 1 : 4) : b + row_x[j] * kRowS);
   };
   WAIT_VM((STAGES - 2) * kPer + first_of(1));
-  asm volatile("s_barrier" ::: "memory");
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
   for (int i = 0; i < FN + FM; ++i) read(0, 0, i);
   read_scales(0, 0);
@@ -353,9 +418,10 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
 
 template <int BM, int BN, int WM, int WN, int KU, int STAGES, int OCC, bool WIDE, int MODE, int DTYPE>
 void run(moe_ctx *ctx, const MxProduct &p, uint8_t *a_scales) {
-  const int64_t units = (p.offsets ? (p.L < p.E ? p.L : p.L / BM + p.E) : (p.L + BM - 1) / BM) + (p.shared + BM - 1) / BM;
+  constexpr int kM = BM ? BM : 1;
+  const int64_t units = (p.offsets ? (p.L < p.E ? p.L : p.L / kM + p.E) : (p.L + kM - 1) / kM) + (p.shared + kM - 1) / kM;
   const int cols = MODE == kGateUp ? BN / 2 : BN;
-  const TileMap m = tile_map(units, (p.N + cols - 1) / cols, p.offsets && p.L <= (int64_t)p.E * BM);
+  const TileMap m = tile_map(units, (p.N + cols - 1) / cols, BM == 0 || (p.offsets && p.L <= (int64_t)p.E * BM));
   auto kernel = mx_tile_kernel<BM, BN, WM, WN, KU, STAGES, OCC, WIDE, MODE, DTYPE>;
   if (MODE == kPlain)
     hipLaunchKernelGGL(kernel, dim3(tile_grid(m)), dim3(WM * WN * 64), 0, ctx->stream, p, m, a_scales);
@@ -456,6 +522,29 @@ moe_status launch_mx_tile_product(moe_ctx *ctx, int dtype, const MxProduct &p) {
 moe_status launch_mx_gateup(moe_ctx *ctx, const MxProduct &p, uint8_t *scales) {
   launch<kGateUp, MOE_FP32>(ctx, p, scales);
   MOE_CHECK_LAUNCH("mx gate/up tile kernel");
+  return MOE_OK;
+}
+#ifndef ONE
+#define ONE 0, 64, 1, 2, 8, 4, 2
+#endif
+template <int MODE, int DTYPE>
+void launch_one(moe_ctx *ctx, const MxProduct &p, uint8_t *a_scales) {
+  if (p.K % (16 * kMxBlock) == 0)
+    run<ONE, true, MODE, DTYPE>(ctx, p, a_scales);
+  else
+    run<ONE, false, MODE, DTYPE>(ctx, p, a_scales);
+}
+moe_status launch_mx_gateup_one(moe_ctx *ctx, const MxProduct &p, uint8_t *scales) {
+  launch_one<kGateUp, MOE_FP32>(ctx, p, scales);
+  MOE_CHECK_LAUNCH("mx gate/up tile kernel");
+  return MOE_OK;
+}
+moe_status launch_mx_down_one(moe_ctx *ctx, int dtype, const MxProduct &p) {
+  if (dtype == MOE_BF16)
+    launch_one<kDown, MOE_BF16>(ctx, p, nullptr);
+  else
+    launch_one<kDown, MOE_FP32>(ctx, p, nullptr);
+  MOE_CHECK_LAUNCH("mx down tile kernel");
   return MOE_OK;
 }
 moe_status launch_mx_down(moe_ctx *ctx, int dtype, const MxProduct &p) {

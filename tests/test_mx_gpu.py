@@ -364,7 +364,10 @@ def check_ffn(out, x, idx, w, experts, E, shared):
                                               (3, 4, 16, 192, 448, True), (33, 2, 5, 256, 128, True),
                                               (70, 3, 9, 448, 320, False), (300, 2, 4, 128, 576, True),
                                               (6, 2, 7, 512, 1024, True), (130, 2, 3, 1536, 512, True),
-                                              (700, 2, 3, 512, 512, False), (900, 1, 2, 192, 320, True)])
+                                              (700, 2, 3, 512, 512, False), (900, 1, 2, 192, 320, True),
+                                              (1, 4, 6, 512, 1536, True), (1, 1, 3, 8192, 64, False),
+                                              (1, 16, 20, 64, 8192, True), (2, 2, 16, 1024, 512, True),
+                                              (3, 1, 12, 192, 1088, False), (2, 3, 24, 8128, 128, True)])
 def test_ffn(moe, ctx, dtype, T, k, E, H, I, shared):
     rng = np.random.default_rng(T + k + E)
     experts = Experts(moe, ctx, T, E + int(shared), H, I)
@@ -381,21 +384,21 @@ def test_ffn(moe, ctx, dtype, T, k, E, H, I, shared):
     check_ffn(out, x, idx, w, experts, E, shared)
 
 
-@pytest.mark.parametrize("T", [1, 5])
-def test_ffn_bad_ids(moe, ctx, T):
+@pytest.mark.parametrize("T,E", [(1, 6), (5, 6), (2, 40)])
+def test_ffn_bad_ids(moe, ctx, T, E):
     """An id out of range and a repeated one add nothing and are reported."""
-    E, k, H, I = 6, 4, 128, 128
+    k, H, I = 4, 128, 128
     experts = Experts(moe, ctx, 1, E + 1, H, I)
     rng = np.random.default_rng(3)
     x = torch.from_numpy(rng.standard_normal((T, H))).float().cuda()
     w = rng.random((T, k)).astype(np.float32)
-    for bad in ([3, 6, -5, 0], [2, 2, 1, 2], [-1, -1, -1, -1]):
+    for bad in ([3, E, -5, 0], [2, 2, 1, 2], [-1, -1, -1, -1], [5, -1, 5, -1], [2 ** 31 - 1, -2 ** 31, 1, 1]):
         idx = np.tile(np.array([0, 1, 2, 3], dtype=np.int32), (T, 1))
         idx[T - 1] = bad
         out = torch.empty_like(x)
         moe.moe_expert_ffn_mx(ctx, experts.blocks.table, True, x, torch.from_numpy(idx).cuda(),
                               torch.from_numpy(w).cuda(), I, out)
-        if bad[0] >= 0:
+        if bad[0] != -1:
             with pytest.raises(moe.MoeError):
                 ctx.check()
         ctx.check()

@@ -135,32 +135,32 @@ extern "C" moe_status moe_expert_ffn_mx(moe_ctx *ctx, int dtype, const moe_mx_ex
   // beside the weights is theirs); fp16 ones are not, since a slot may pass fp16's range where the sum does not
   const int y_dtype = dtype == MOE_BF16 ? MOE_BF16 : MOE_FP32;
   const int64_t routed = (int64_t)T * k, lines = routed + (has_shared ? T : 0);
-  // a line a unit saves the bucketing and, with it, two launches (9 + 4 us); tokens that share experts read them twice
-  const bool one = T == 1 || (T <= 3 && E >= 4 * T * k);
-  MoeLayout l;
-  const size_t o_a = l.take((size_t)lines * I / 2), o_sa = l.take((size_t)lines * I / kMxBlock),
-               o_y = l.take((size_t)lines * H * (y_dtype == MOE_BF16 ? 2 : 4)), o_x = l.take(one ? 0 : (size_t)T * H / 2),
-               o_sx = l.take(one ? 0 : (size_t)T * H / kMxBlock), o_counts = l.take(one ? 0 : 4 * E),
-               o_offsets = l.take(one ? 0 : 4 * (E + 1)), o_perm = l.take(one ? 0 : 4 * routed);
   void *scr = nullptr;
+  MoeLayout l;
+  const size_t o_a = l.take((size_t)lines * I / 2), o_sa = l.take((size_t)lines * I / kMxBlock);
+  // slot by slot: no bucketing, no launches for the quantiser and the combine; tokens that share experts read them twice
+  if (T == 1 || (T <= 3 && E >= 4 * T * k)) {
+    if ((st = moe_scratch(ctx, l.size, &scr))) return st;
+    uint8_t *b = static_cast<uint8_t *>(scr);
+    return launch_mx_one(ctx, MxOne{x, dtype, experts, topk_idx, topk_w, T, H, I, E, k, has_shared ? 1 : 0, b + o_a, b + o_sa,
+                                    out, ctx->dev_small});
+  }
+  const size_t o_y = l.take((size_t)lines * H * (y_dtype == MOE_BF16 ? 2 : 4)), o_x = l.take((size_t)T * H / 2),
+               o_sx = l.take((size_t)T * H / kMxBlock), o_counts = l.take(4 * E), o_offsets = l.take(4 * (E + 1)),
+               o_perm = l.take(4 * routed);
   if ((st = moe_scratch(ctx, l.size, &scr))) return st;
   uint8_t *b = static_cast<uint8_t *>(scr);
+  int32_t *offsets = reinterpret_cast<int32_t *>(b + o_offsets), *perm = reinterpret_cast<int32_t *>(b + o_perm);
+  if ((st = launch_mx_quantize(ctx, dtype, x, T, H, H, b + o_x, b + o_sx))) return st;
+  if ((st = launch_bucket_public(ctx, topk_idx, T, k, E, reinterpret_cast<int32_t *>(b + o_counts), offsets, perm)))
+    return st;
   MxProduct p{};
-  p.x = static_cast<const uint8_t *>(x), p.X = T, p.table = experts, p.N = I, p.K = H, p.E = E, p.L = routed, p.k = k;
-  p.shared = has_shared ? T : 0, p.tokens = true, p.out = b + o_a, p.R = lines, p.err = ctx->dev_small;
-  if (one) {
-    p.ids = topk_idx, p.per_token = k, p.x_dtype = dtype;
-    if ((st = launch_mx_gateup_one(ctx, p, b + o_sa))) return st;
-  } else {
-    int32_t *offsets = reinterpret_cast<int32_t *>(b + o_offsets), *perm = reinterpret_cast<int32_t *>(b + o_perm);
-    if ((st = launch_mx_quantize(ctx, dtype, x, T, H, H, b + o_x, b + o_sx))) return st;
-    if ((st = launch_bucket_public(ctx, topk_idx, T, k, E, reinterpret_cast<int32_t *>(b + o_counts), offsets, perm)))
-      return st;
-    p.x = b + o_x, p.sx = b + o_sx, p.offsets = offsets, p.in_rows = perm;
-    if ((st = launch_mx_gateup(ctx, p, b + o_sa))) return st;
-  }
+  p.x = b + o_x, p.sx = b + o_sx, p.X = T, p.table = experts, p.N = I, p.K = H, p.E = E, p.L = routed, p.k = k;
+  p.offsets = offsets, p.in_rows = perm, p.shared = has_shared ? T : 0, p.tokens = true;
+  p.out = b + o_a, p.R = lines, p.err = ctx->dev_small;
+  if ((st = launch_mx_gateup(ctx, p, b + o_sa))) return st;
   p.x = b + o_a, p.sx = b + o_sa, p.X = lines, p.N = H, p.K = I, p.tokens = false;
   p.out_rows = p.in_rows, p.in_rows = nullptr, p.out = b + o_y;
-  if ((st = one ? launch_mx_down_one(ctx, y_dtype, p) : launch_mx_down(ctx, y_dtype, p))) return st;
+  if ((st = launch_mx_down(ctx, y_dtype, p))) return st;
   return launch_mx_combine(ctx, y_dtype, dtype, b + o_y, topk_idx, topk_w, T, k, E, H, has_shared, out);
 }

@@ -6,6 +6,8 @@
 // codes are 16 bytes, what one lane gives to a matrix instruction.
 #pragma once
 
+#include <type_traits>
+
 #include "moe_internal.h"
 
 constexpr int kMxBlock = 32;
@@ -19,17 +21,14 @@ struct MxProduct {
   int64_t w_e, sw_e;
   const moe_mx_expert_w *table;
   int N, K;
-  // lines: line l is row in_rows[l] / k of x (NULL: l / k) and goes to row out_rows[l] of out (NULL: l)
+  // lines: line l is row in_rows[l] / k of x (NULL: l) and goes to row out_rows[l] of out (NULL: l)
   const int32_t *offsets;  // [E + 1], expert e's lines are offsets[e] ..; NULL: one expert has all L of them
-  const int32_t *ids;      // or line l is expert ids[l]'s, none's if that is no expert or one of token l / per_token's earlier lines
-  int per_token;
   int E;
   int64_t L;
   const int32_t *in_rows, *out_rows;
   int k;
   int64_t shared;  // lines L .. L + shared - 1 are expert E's and rows 0 .. of x where `tokens`, else rows L ..
   bool tokens;     // x has a row a token
-  int x_dtype;     // gate/up with ids: x is values of this type and sx unused
   void *out;
   int64_t R;  // rows of out
   uint32_t *err;
@@ -44,9 +43,20 @@ bool mx_tiles(const moe_ctx *ctx, const MxProduct &p);
 // out = x w^T line by line
 moe_status launch_mx_product(moe_ctx *ctx, int dtype, const MxProduct &p);
 moe_status launch_mx_tile_product(moe_ctx *ctx, int dtype, const MxProduct &p);
-// The same for one line a unit (ids): gate/up's x is then values, quantised by every workgroup for itself.
-moe_status launch_mx_gateup_one(moe_ctx *ctx, const MxProduct &p, uint8_t *scales);
-moe_status launch_mx_down_one(moe_ctx *ctx, int dtype, const MxProduct &p);
+// The experts' FFN of T tokens on hidden states x of x_dtype, each slot by itself: gate and up into lines (codes a and
+// scales sa, slot by slot, then the shared expert's), then down with the combine into out.
+struct MxOne {
+  const void *x;
+  int dtype;
+  const moe_mx_expert_w *table;
+  const int32_t *idx;
+  const float *w;
+  int T, H, I, E, k, shared;
+  uint8_t *a, *sa;
+  void *out;
+  uint32_t *err;
+};
+moe_status launch_mx_one(moe_ctx *ctx, const MxOne &p);
 // silu(x gate^T) * (x up^T) line by line (the table's gate and up), in 4 bits: out's row l is line l
 moe_status launch_mx_gateup(moe_ctx *ctx, const MxProduct &p, uint8_t *scales);
 // the table's down
@@ -157,6 +167,50 @@ __device__ __forceinline__ f32x4 mx_mfma16(i32x4 a, int sa, i32x4 b, int sb, f32
                                                           4, 4, 0, sa, 0, sb);
 }
 
+// f(integral_constant<int, A>) .. f(integral_constant<int, B - 1>)
+template <int A, int B, typename F>
+__device__ __forceinline__ void mx_static_for(F &&f) {
+  if constexpr (A < B) {
+    f(std::integral_constant<int, A>{});
+    mx_static_for<A + 1, B>(f);
+  }
+}
+
+// c += a b^T: lane l holds 32 k of row l % 32 of a and of b, block l / 32 of two, and byte S of sa and sb is its scale; of
+// c it holds column l % 32 (b's row), rows 8 (i / 4) + 4 (l / 32) + i % 4.
+template <int S>
+__device__ __forceinline__ f32x16 mx_mfma32(i32x4 a, int sa, i32x4 b, int sb, f32x16 c) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(__builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1),
+                                                         __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1), c,
+                                                         4, 4, S, sa, S, sb);
+}
+
+static __device__ __attribute__((aligned(16))) const uint8_t mx_zeros[16] = {};
+
+// 16 bytes a lane from global memory straight into LDS, in order of lanes from byte `to` on; on, high: -1, or 0 for a load
+// that moves nothing but is counted all the same, for the lower and the upper 32 lanes. In assembly so that the compiler does not wait for it; the kernel waits
+// by count (vmcnt). All lanes must be active.
+__device__ __forceinline__ void mx_lds_load16(const void *p, uint32_t to, int on, int high) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b32 exec_lo, %2\n\ts_mov_b32 exec_hi, %3\n\t"
+               "global_load_lds_dwordx4 %0, off\n\ts_mov_b64 exec, -1" ::"v"(p), "s"(to), "s"(on), "s"(high)
+               : "memory");
+}
+// -1 where a < b, else 0, in a scalar register: computed from a comparison, the compiler has been seen to hand the
+// assembly above a vector register.
+__device__ __forceinline__ int mx_below(int a, int b) {
+  int r;
+  asm("s_cmp_lt_i32 %1, %2\n\ts_cselect_b32 %0, -1, 0" : "=s"(r) : "s"(a), "s"(b) : "scc");
+  return r;
+}
+// The same for a byte a lane, each into a word.
+__device__ __forceinline__ void mx_lds_load1(const void *p, uint32_t to, int on) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b32 exec_lo, %2\n\ts_mov_b32 exec_hi, %2\n\t"
+               "global_load_lds_ubyte %0, off\n\ts_mov_b64 exec, -1" ::"v"(p), "s"(to), "s"(on)
+               : "memory");
+}
+// s_waitcnt vmcnt(n) alone
+#define WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (((n) >> 4) << 14) | (7 << 4) | (15 << 8))
+
 // A unit of work: up to `tile` lines of one expert.
 struct MxUnit {
   int e;           // expert; E for the shared one
@@ -230,16 +284,6 @@ __device__ __forceinline__ MxUnit mx_unit(const MxProduct &p, int64_t u) {
   return r;
 }
 
-// Unit u where each line is one: p.ids' lines, then the shared expert's.
-__device__ __forceinline__ MxUnit mx_unit_one(const MxProduct &p, int u) {
-  if (u >= p.L) return MxUnit{p.E, u, u < p.L + p.shared ? 1 : 0};
-  const int id = p.ids[u];
-  bool ok = id >= 0 && id < p.E;
-  for (int i = u / p.per_token * p.per_token; i < u; ++i) ok &= p.ids[i] != id;
-  if (!ok && id != -1) atomicOr(p.err, (uint32_t)ERRF_BAD_INDEX);
-  return MxUnit{mx_uniform(id), u, mx_uniform(ok ? 1 : 0)};
-}
-
 // Row of x of a line, and where its result goes; -1: out of range, which is reported.
 __device__ __forceinline__ int64_t mx_in_row(const MxProduct &p, int64_t line) {
   int64_t r = line;
@@ -247,8 +291,6 @@ __device__ __forceinline__ int64_t mx_in_row(const MxProduct &p, int64_t line) {
     r = line - p.L;
   else if (p.in_rows)
     r = p.in_rows[line] / p.k;
-  else if (p.tokens)
-    r = line / p.k;
   if (r >= 0 && r < p.X) return r;
   atomicOr(p.err, (uint32_t)ERRF_MX);
   return -1;

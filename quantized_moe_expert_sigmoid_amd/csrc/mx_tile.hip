@@ -14,10 +14,6 @@
 // lane reads the word it needs and the instruction picks a byte. Other rows' scales
 // come a byte a lane, each into a word of its own.
 //
-// BM = 0 is for one line a unit: its codes lie in LDS from the start (for gate/up the
-// workgroup makes them from the values, while it waits for the expert's addresses),
-// all columns of a product are that line, and only weights come stage by stage.
-//
 // A wave has the operands of the next product step in registers before the
 // present one begins, and a stage's place is loaded again while its last products
 // run: STAGES - 1 stages are in flight.
@@ -29,46 +25,7 @@
 
 namespace {
 
-__device__ __attribute__((aligned(16))) const uint8_t mx_zeros[16] = {};
-
-// 16 bytes a lane from global memory straight into LDS, in order of lanes from byte `to` on; on: -1, or 0 for a load
-// that moves nothing but is counted all the same. In assembly so that the compiler does not wait for it; the kernel waits
-// by count (vmcnt). All lanes must be active.
-__device__ __forceinline__ void lds_load16(const void *p, uint32_t to, int on) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b32 exec_lo, %2\n\ts_mov_b32 exec_hi, %2\n\t"
-               "global_load_lds_dwordx4 %0, off\n\ts_mov_b64 exec, -1" ::"v"(p), "s"(to), "s"(on)
-               : "memory");
-}
-// The same for a byte a lane, each into a word.
-__device__ __forceinline__ void lds_load1(const void *p, uint32_t to, int on) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b32 exec_lo, %2\n\ts_mov_b32 exec_hi, %2\n\t"
-               "global_load_lds_ubyte %0, off\n\ts_mov_b64 exec, -1" ::"v"(p), "s"(to), "s"(on)
-               : "memory");
-}
-// s_waitcnt vmcnt(n) alone
-#define WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (((n) >> 4) << 14) | (7 << 4) | (15 << 8))
-
-// f(integral_constant<int, A>) .. f(integral_constant<int, B - 1>)
-template <int A, int B, typename F>
-__device__ __forceinline__ void static_for(F &&f) {
-  if constexpr (A < B) {
-    f(std::integral_constant<int, A>{});
-    static_for<A + 1, B>(f);
-  }
-}
-
-// c += a b^T: lane l holds 32 k of row l % 32 of a and of b, block l / 32 of two, and byte S of sa and sb is its scale; of
-// c it holds column l % 32 (b's row), rows 8 (i / 4) + 4 (l / 32) + i % 4.
-template <int S>
-__device__ __forceinline__ f32x16 mfma32(i32x4 a, int sa, i32x4 b, int sb, f32x16 c) {
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(__builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1),
-                                                         __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1), c,
-                                                         4, 4, S, sa, S, sb);
-}
-
 enum { kPlain, kDown, kGateUp };
-
-constexpr int kOneK = 8192;  // the longest row of one-line units
 
 // How workgroups map to tiles: blocks of g units x gn column tiles go round the 8 XCDs; within one, units run fastest.
 // With a unit an expert nothing is shared but a few lines, and single tiles go round, so that all XCDs have as many (one
@@ -91,8 +48,7 @@ unsigned tile_grid(const TileMap &m) {
 template <int BM, int BN, int WM, int WN, int KU, int STAGES, int OCC, bool WIDE, int MODE, int DTYPE>
 __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, TileMap map, uint8_t *a_scales) {
   typedef MxOut<DTYPE> O;
-  constexpr bool kOne = BM == 0;
-  constexpr int kWaves = WM * WN, FM = kOne ? 1 : BM / WM / 32, FN = BN / WN / 32;
+  constexpr int kWaves = WM * WN, FM = BM / WM / 32, FN = BN / WN / 32;
   constexpr int kRows = BM + BN, kRowB = KU * 16, kStage = kRows * kRowB, kAt = STAGES * kStage;
   // scales: stages of a load, loads kept, bytes of one
   constexpr int kChunk = WIDE ? 16 / KU : 1, kChunks = (STAGES + kChunk - 2) / kChunk + 1, kScales = kRows * (WIDE ? 16 : 4 * KU);
@@ -101,71 +57,15 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
   constexpr int kCols = MODE == kGateUp ? BN / 2 : BN;  // of the result
   static_assert(kRows % (kRowsL * kWaves) == 0 && kWaves * kRowsL % 16 == 0 && (KU == 4 || KU == 8));
   static_assert(MODE != kGateUp || FN % 2 == 0 || (FN == 1 && WN % 2 == 0));
-  // one line's codes and scales (in bytes, or words), and a stage more, which is read but not used
-  constexpr int kLine = kAt + kChunks * kScales, kLineS = kLine + kOneK / 2 + kRowB, kLineEnd = kLineS + (kOneK / 32 + KU) * (WIDE ? 1 : 4);
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kOne ? kLineEnd : kLine];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kAt + kChunks * kScales];
 
   const int xcd = blockIdx.x & 7, j0 = blockIdx.x >> 3, per_block = map.g * map.gn;
   const int block = j0 / per_block * 8 + xcd, rest = j0 % per_block, across = (map.n_tiles + map.gn - 1) / map.gn;
   const int unit = block / across * map.g + rest % map.g, nt = block % across * map.gn + rest / map.g;
   if (unit >= map.units || nt >= map.n_tiles) return;
   const int n0 = nt * kCols, blocks = p.K / kMxBlock, steps = (blocks + KU - 1) / KU;
-  MxUnit u;
-  if constexpr (kOne) {
-    constexpr int kChunk8 = kOneK / 8 / (kWaves * 64);  // words of eight codes a thread
-    const int64_t row = p.tokens ? (unit < p.L ? unit / p.k : unit - p.L) : unit;
-    uint32_t code[kChunk8], byte[kChunk8];
-    if constexpr (MODE == kGateUp) {
-      float v[kChunk8][8];
-      auto values = [&](auto type) {
-        typedef typename MxOut<decltype(type)::value>::T T;
-#pragma unroll
-        for (int i = 0; i < kChunk8; ++i) {
-          const int c = i * kWaves * 64 + threadIdx.x;
-          if (c < blocks * 4) mx_load8<decltype(type)::value>(reinterpret_cast<const T *>(p.x) + row * p.K + c * 8, v[i]);
-        }
-      };
-      if (p.x_dtype == MOE_FP32)
-        values(std::integral_constant<int, MOE_FP32>{});
-      else if (p.x_dtype == MOE_BF16)
-        values(std::integral_constant<int, MOE_BF16>{});
-      else
-        values(std::integral_constant<int, MOE_FP16>{});
-      u = mx_unit_one(p, unit);
-      if (u.n == 0) return;
-#pragma unroll
-      for (int i = 0; i < kChunk8; ++i)
-        if (i * kWaves * 64 + threadIdx.x < blocks * 4) code[i] = mx_codes8(v[i], byte[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kChunk8; ++i) {
-        const int c = i * kWaves * 64 + threadIdx.x;
-        if (c < blocks * 4) {
-          code[i] = reinterpret_cast<const uint32_t *>(p.x)[row * blocks * 4 + c];
-          byte[i] = p.sx[row * blocks + c / 4];
-        }
-      }
-      u = mx_unit_one(p, unit);
-      if (u.n == 0) return;
-    }
-#pragma unroll
-    for (int i = 0; i < kChunk8; ++i) {
-      const int c = i * kWaves * 64 + threadIdx.x;
-      if (c < steps * KU * 4) {  // zeros behind the row's end
-        reinterpret_cast<uint32_t *>(lds + kLine)[c] = c < blocks * 4 ? code[i] : 0;
-        const uint32_t s = c < blocks * 4 ? byte[i] : 0;
-        if ((c & 3) == 0) {
-          if constexpr (WIDE)
-            lds[kLineS + c / 4] = (uint8_t)s;
-          else
-            reinterpret_cast<uint32_t *>(lds + kLineS)[c / 4] = s;
-        }
-      }
-    }
-  } else {
-    u = mx_unit<BM>(p, unit);
-    if (u.n == 0) return;
-  }
+  const MxUnit u = mx_unit<BM>(p, unit);
+  if (u.n == 0) return;
   const int lane = threadIdx.x & 63, wave = mx_uniform((int)(threadIdx.x >> 6)), l32 = lane & 31, hl = lane >> 5;
   const int wm = wave % WM, wn = wave / WM;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
@@ -189,9 +89,9 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
   auto w_row = [&](int n) { return (int64_t)min(n0 + n, p.N - 1) * blocks; };
   const int mine = (lane % KU) ^ swz((wave * kRowsL + lane / KU) & 15);  // the unit of its row that a lane loads
   const uint8_t *src[kLoads], *src_s[kLoadsS];
-  static_for<0, kLoads>([&](auto ic) {
+  mx_static_for<0, kLoads>([&](auto ic) {
     constexpr int first = decltype(ic)::value * kWaves * kRowsL, n = first - BM;
-    static_assert((kOne || BM % (kWaves * kRowsL) == 0) && kCols % (kWaves * kRowsL) == 0);
+    static_assert(BM % (kWaves * kRowsL) == 0 && kCols % (kWaves * kRowsL) == 0);
     const int r = wave * kRowsL + lane / KU;
     if constexpr (n < 0)
       src[ic] = p.x + (x_row(first + r) + mine) * 16;
@@ -207,18 +107,18 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
   // piece i of stage s: rows of codes, then of scales. Sources go on by a stage each time they are used; those of the
   // last stage, if it is not whole, are zeros where a row ends.
   auto load = [&](int s, int i) {
-    const int on = mx_uniform(s < steps ? -1 : 0);
+    const int on = mx_below(mx_uniform(s), mx_uniform(steps));
     if (i < kLoads) {
-      lds_load16(src[i], mx_uniform((int)(lds0 + s % STAGES * kStage + (i * kWaves + wave) * 1024)), on);
+      mx_lds_load16(src[i], mx_uniform((int)(lds0 + s % STAGES * kStage + (i * kWaves + wave) * 1024)), on, on);
       src[i] += kRowB;
     } else {
       const int j = i - kLoads, r = (j * kWaves + wave) * kRowsS;
       const int to = mx_uniform((int)(lds0 + kAt + s / kChunk % kChunks * kScales + min(r, kRows - kRowsS) * (kScales / kRows)));
-      const int on_s = mx_uniform(r < kRows && s % kChunk == 0 ? on : 0);
+      const int on_s = on & mx_below(r, kRows) & mx_below(s % kChunk, 1);
       if constexpr (WIDE)
-        lds_load16(src_s[j], to, on_s);
+        mx_lds_load16(src_s[j], to, on_s, on_s);
       else
-        lds_load1(src_s[j], to, on_s);
+        mx_lds_load1(src_s[j], to, on_s);
       src_s[j] += KU;
     }
   };
@@ -266,8 +166,6 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
     const uint8_t *b = lds + s % STAGES * kStage + off[k];
     if (i < FN)
       wf[k & 1][i] = *reinterpret_cast<const i32x4 *>(b + row_w[i] * kRowB);
-    else if (kOne)
-      xf[k & 1][0] = *reinterpret_cast<const i32x4 *>(lds + kLine + s * kRowB + (KU / 2 * hl + k) * 16);
     else
       xf[k & 1][i - FN] = *reinterpret_cast<const i32x4 *>(b + row_x[i - FN] * kRowB);
   };
@@ -278,17 +176,16 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
 #pragma unroll
     for (int i = 0; i < FN; ++i) ws[to][i] = *reinterpret_cast<const Scale *>(b + row_w[i] * kRowS);
 #pragma unroll
-    for (int j = 0; j < FM; ++j)
-      xs[to][j] = *reinterpret_cast<const Scale *>(kOne ? lds + kLineS + (s * KU + KU / 2 * hl) * (WIDE ? 1 : 4) : b + row_x[j] * kRowS);
+    for (int j = 0; j < FM; ++j) xs[to][j] = *reinterpret_cast<const Scale *>(b + row_x[j] * kRowS);
   };
   WAIT_VM((STAGES - 2) * kPer + first_of(1));
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("s_barrier" ::: "memory");
 #pragma unroll
   for (int i = 0; i < FN + FM; ++i) read(0, 0, i);
   read_scales(0, 0);
   auto stage = [&](int s, auto parity) {
     constexpr int P = decltype(parity)::value;
-    static_for<0, kSteps>([&](auto kc) {
+    mx_static_for<0, kSteps>([&](auto kc) {
       constexpr int k = decltype(kc)::value, kPhase = (k + 1) % kSteps;
       const int s_load = s + STAGES - (kPhase ? 1 : 0);
       if constexpr (kPhase == 0) {  // this stage is read, the next one is there, for every wave
@@ -299,12 +196,12 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
       __builtin_amdgcn_sched_barrier(0);
       // Between the products: the next step's operands, in the first half of them, and the loads.
       constexpr int F = FN * FM, kHalf = F > 1 ? F / 2 : 1, R = FN + FM, kBegin = first_of(kPhase), kNum = first_of(kPhase + 1) - kBegin;
-      static_for<0, F>([&](auto tc) {
+      mx_static_for<0, F>([&](auto tc) {
         constexpr int t = decltype(tc)::value, i = t / FM, j = t % FM;
         if constexpr (WIDE)
-          acc[i][j] = mfma32<k>(wf[k & 1][i], ws[P][i], xf[k & 1][j], xs[P][j], acc[i][j]);
+          acc[i][j] = mx_mfma32<k>(wf[k & 1][i], ws[P][i], xf[k & 1][j], xs[P][j], acc[i][j]);
         else
-          acc[i][j] = mfma32<0>(wf[k & 1][i], ws[P][i][k], xf[k & 1][j], xs[P][j][k], acc[i][j]);
+          acc[i][j] = mx_mfma32<0>(wf[k & 1][i], ws[P][i][k], xf[k & 1][j], xs[P][j][k], acc[i][j]);
         if constexpr (t < kHalf) {
 #pragma unroll
           for (int r = t * R / kHalf; r < (t + 1) * R / kHalf; ++r) read(kPhase ? s : s + 1, kPhase, r);
@@ -418,10 +315,9 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
 
 template <int BM, int BN, int WM, int WN, int KU, int STAGES, int OCC, bool WIDE, int MODE, int DTYPE>
 void run(moe_ctx *ctx, const MxProduct &p, uint8_t *a_scales) {
-  constexpr int kM = BM ? BM : 1;
-  const int64_t units = (p.offsets ? (p.L < p.E ? p.L : p.L / kM + p.E) : (p.L + kM - 1) / kM) + (p.shared + kM - 1) / kM;
+  const int64_t units = (p.offsets ? (p.L < p.E ? p.L : p.L / BM + p.E) : (p.L + BM - 1) / BM) + (p.shared + BM - 1) / BM;
   const int cols = MODE == kGateUp ? BN / 2 : BN;
-  const TileMap m = tile_map(units, (p.N + cols - 1) / cols, BM == 0 || (p.offsets && p.L <= (int64_t)p.E * BM));
+  const TileMap m = tile_map(units, (p.N + cols - 1) / cols, p.offsets && p.L <= (int64_t)p.E * BM);
   auto kernel = mx_tile_kernel<BM, BN, WM, WN, KU, STAGES, OCC, WIDE, MODE, DTYPE>;
   if (MODE == kPlain)
     hipLaunchKernelGGL(kernel, dim3(tile_grid(m)), dim3(WM * WN * 64), 0, ctx->stream, p, m, a_scales);
@@ -522,29 +418,6 @@ moe_status launch_mx_tile_product(moe_ctx *ctx, int dtype, const MxProduct &p) {
 moe_status launch_mx_gateup(moe_ctx *ctx, const MxProduct &p, uint8_t *scales) {
   launch<kGateUp, MOE_FP32>(ctx, p, scales);
   MOE_CHECK_LAUNCH("mx gate/up tile kernel");
-  return MOE_OK;
-}
-#ifndef ONE
-#define ONE 0, 64, 1, 2, 8, 4, 2
-#endif
-template <int MODE, int DTYPE>
-void launch_one(moe_ctx *ctx, const MxProduct &p, uint8_t *a_scales) {
-  if (p.K % (16 * kMxBlock) == 0)
-    run<ONE, true, MODE, DTYPE>(ctx, p, a_scales);
-  else
-    run<ONE, false, MODE, DTYPE>(ctx, p, a_scales);
-}
-moe_status launch_mx_gateup_one(moe_ctx *ctx, const MxProduct &p, uint8_t *scales) {
-  launch_one<kGateUp, MOE_FP32>(ctx, p, scales);
-  MOE_CHECK_LAUNCH("mx gate/up tile kernel");
-  return MOE_OK;
-}
-moe_status launch_mx_down_one(moe_ctx *ctx, int dtype, const MxProduct &p) {
-  if (dtype == MOE_BF16)
-    launch_one<kDown, MOE_BF16>(ctx, p, nullptr);
-  else
-    launch_one<kDown, MOE_FP32>(ctx, p, nullptr);
-  MOE_CHECK_LAUNCH("mx down tile kernel");
   return MOE_OK;
 }
 moe_status launch_mx_down(moe_ctx *ctx, int dtype, const MxProduct &p) {

@@ -581,26 +581,28 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 def _dtype(t: torch.Tensor, name):
-    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
-        raise TypeError(f"{name} must be a bfloat16, float16 or float32 tensor")
-    return _DTYPES[t.dtype]
+    try:
+        return _DTYPES[t.dtype]
+    except (AttributeError, KeyError):
+        raise TypeError(f"{name} must be a bfloat16, float16 or float32 tensor") from None
 
 
-def _on(ctx: MoeCtx, t: torch.Tensor, dtype, name, shape=None):
-    """_dev, on the context's device."""
-    p = _dev(t, dtype, name, shape)
-    if t.device.index != ctx.device:
-        raise ValueError(f"{name} is on {t.device}, the context on device {ctx.device}")
-    return p
+def _at(ctx: MoeCtx, t: torch.Tensor, dtype, shape, name):
+    """Address of a contiguous tensor of this type and shape on the context's
+    device (small calls are bound by the host: what is right costs one line)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == ctx.device \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, dtype, name, torch.Size(shape))
+    raise ValueError(f"{name} is on {t.device}, the context on device {ctx.device}")
 
 
-def _mx(ctx, codes, scales, name):
-    """A matrix as codes [..., K / 2] and scales [..., K / 32]: (codes' address, scales', K)."""
-    c = _on(ctx, codes, torch.uint8, f"{name} codes")
-    K = 2 * codes.shape[-1]
-    if K % 32:
-        raise ValueError(f"{name} codes: rows of {K} values are no whole blocks of 32")
-    return c, _on(ctx, scales, torch.uint8, f"{name} scales", (*codes.shape[:-1], K // 32)), K
+def _blocks(t: torch.Tensor, dims: int, name):
+    """Shape of codes [..., K / 2], whole blocks of 32."""
+    shape = t.shape
+    if len(shape) != dims or shape[-1] % 16:
+        raise ValueError(f"{name} codes: {tuple(shape)} is not {dims} dimensions of whole blocks of 32 (16 bytes)")
+    return shape
 
 
 def moe_mx_quantize(ctx: MoeCtx, x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
@@ -608,28 +610,30 @@ def moe_mx_quantize(ctx: MoeCtx, x: torch.Tensor, codes: torch.Tensor, scales: t
     float32 (rows may be strided), codes uint8 [rows][K / 2], scales uint8
     [rows][K / 32]."""
     dtype = _dtype(x, "x")
-    if not x.is_cuda or x.device.index != ctx.device:
-        raise TypeError(f"x must be on device {ctx.device}")
+    if x.get_device() != ctx.device:
+        raise TypeError(f"x must be on device {ctx.device}, it is on {x.device}")
     if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
         raise ValueError("x must be [rows][K] with contiguous rows")
     rows, K = x.shape
     if K % 32:
         raise ValueError(f"x: rows of {K} values are no whole blocks of 32")
-    _ck(lib().moe_mx_quantize(ctx.handle, dtype, x.data_ptr(), rows, K, x.stride(0) if rows > 1 else K,
-                              _on(ctx, codes, torch.uint8, "codes", (rows, K // 2)),
-                              _on(ctx, scales, torch.uint8, "scales", (rows, K // 32))))
+    st = lib().moe_mx_quantize(ctx.handle, dtype, x.data_ptr(), rows, K, x.stride(0) if rows > 1 else K,
+                               _at(ctx, codes, torch.uint8, (rows, K // 2), "codes"),
+                               _at(ctx, scales, torch.uint8, (rows, K // 32), "scales"))
+    if st:
+        _ck(st)
     return codes, scales
 
 
 def moe_mx_dequantize(ctx: MoeCtx, codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor):
     """What codes [rows][K / 2] and scales [rows][K / 32] stand for, in out
     [rows][K] (bfloat16, float16 or float32)."""
-    c, s, K = _mx(ctx, codes, scales, "")
-    if codes.dim() != 2:
-        raise ValueError("codes must be [rows][K / 2]")
-    rows = codes.shape[0]
-    _ck(lib().moe_mx_dequantize(ctx.handle, _dtype(out, "out"), c, s, rows, K,
-                                _on(ctx, out, out.dtype, "out", (rows, K))))
+    rows, half = shape = _blocks(codes, 2, "")
+    st = lib().moe_mx_dequantize(ctx.handle, _dtype(out, "out"), _at(ctx, codes, torch.uint8, shape, "codes"),
+                                 _at(ctx, scales, torch.uint8, (rows, half // 16), "scales"), rows, 2 * half,
+                                 _at(ctx, out, out.dtype, (rows, 2 * half), "out"))
+    if st:
+        _ck(st)
     return out
 
 
@@ -637,13 +641,17 @@ def moe_mx_matmul(ctx: MoeCtx, x: torch.Tensor, sx: torch.Tensor, w: torch.Tenso
                   out: torch.Tensor):
     """out [M][N] = x w^T (see include/moe.h): codes x [M][K / 2] and w [N][K / 2]
     with their scales; out bfloat16, float16 or float32."""
-    xp, sxp, K = _mx(ctx, x, sx, "x")
-    wp, swp, Kw = _mx(ctx, w, sw, "w")
-    if x.dim() != 2 or w.dim() != 2 or K != Kw:
-        raise ValueError(f"x {tuple(x.shape)} and w {tuple(w.shape)} must be [M][K / 2] and [N][K / 2]")
-    M, N = x.shape[0], w.shape[0]
-    _ck(lib().moe_mx_matmul(ctx.handle, _dtype(out, "out"), xp, sxp, M, wp, swp, N, K,
-                            _on(ctx, out, out.dtype, "out", (M, N))))
+    M, half = xs = _blocks(x, 2, "x")
+    N, half_w = ws = _blocks(w, 2, "w")
+    if half != half_w:
+        raise ValueError(f"x has rows of {2 * half} values, w of {2 * half_w}")
+    u8 = torch.uint8
+    st = lib().moe_mx_matmul(ctx.handle, _dtype(out, "out"), _at(ctx, x, u8, xs, "x codes"),
+                             _at(ctx, sx, u8, (M, half // 16), "x scales"), M, _at(ctx, w, u8, ws, "w codes"),
+                             _at(ctx, sw, u8, (N, half // 16), "w scales"), N, 2 * half,
+                             _at(ctx, out, out.dtype, (M, N), "out"))
+    if st:
+        _ck(st)
     return out
 
 
@@ -654,17 +662,21 @@ def moe_mx_grouped_matmul(ctx: MoeCtx, x: torch.Tensor, sx: torch.Tensor, w: tor
     [E][N][K / 2], offsets int32 [E + 1], out [R][N]; in_rows and out_rows int32
     [lines]: each line's row of x and of out (None: its own number). Without
     either there are as many lines as the smaller of X and R."""
-    xp, sxp, K = _mx(ctx, x, sx, "x")
-    wp, swp, Kw = _mx(ctx, w, sw, "w")
-    if x.dim() != 2 or w.dim() != 3 or K != Kw:
-        raise ValueError(f"x {tuple(x.shape)} and w {tuple(w.shape)} must be [X][K / 2] and [E][N][K / 2]")
-    (E, N), X, R = w.shape[:2], x.shape[0], out.shape[0]
+    X, half = xs = _blocks(x, 2, "x")
+    E, N, half_w = ws = _blocks(w, 3, "w")
+    if half != half_w:
+        raise ValueError(f"x has rows of {2 * half} values, w of {2 * half_w}")
+    R, u8, i32 = out.shape[0], torch.uint8, torch.int32
     L = min(X, R) if in_rows is None and out_rows is None else (out_rows if in_rows is None else in_rows).shape[0]
-    ip = None if in_rows is None else _on(ctx, in_rows, torch.int32, "in_rows", (L,))
-    op = None if out_rows is None else _on(ctx, out_rows, torch.int32, "out_rows", (L,))
-    _ck(lib().moe_mx_grouped_matmul(ctx.handle, _dtype(out, "out"), xp, sxp, X, wp, swp, E, N, K,
-                                    _on(ctx, offsets, torch.int32, "offsets", (E + 1,)), L, ip, op,
-                                    _on(ctx, out, out.dtype, "out", (R, N)), R))
+    st = lib().moe_mx_grouped_matmul(ctx.handle, _dtype(out, "out"), _at(ctx, x, u8, xs, "x codes"),
+                                     _at(ctx, sx, u8, (X, half // 16), "x scales"), X, _at(ctx, w, u8, ws, "w codes"),
+                                     _at(ctx, sw, u8, (E, N, half // 16), "w scales"), E, N, 2 * half,
+                                     _at(ctx, offsets, i32, (E + 1,), "offsets"), L,
+                                     None if in_rows is None else _at(ctx, in_rows, i32, (L,), "in_rows"),
+                                     None if out_rows is None else _at(ctx, out_rows, i32, (L,), "out_rows"),
+                                     _at(ctx, out, out.dtype, (R, N), "out"), R)
+    if st:
+        _ck(st)
     return out
 
 
@@ -674,14 +686,14 @@ def moe_expert_ffn_mx(ctx: MoeCtx, table: torch.Tensor, has_shared: bool, x: tor
     int64 [E][6] of moe_mx_expert_w (with has_shared a further row, the shared
     expert), x and out [T][H] of one type (bfloat16, float16 or float32),
     topk_idx int32 and topk_w float32 [T][k]."""
-    T, H = x.shape
-    k = topk_idx.shape[1]
-    rows = table.shape[0]
-    _ck(lib().moe_expert_ffn_mx(ctx.handle, _dtype(x, "x"), _on(ctx, table, torch.int64, "experts table", (rows, 6)),
-                                1 if has_shared else 0, _on(ctx, x, x.dtype, "x"),
-                                _on(ctx, topk_idx, torch.int32, "topk_idx", (T, k)),
-                                _on(ctx, topk_w, torch.float32, "topk_w", (T, k)), T, H, I,
-                                rows - (1 if has_shared else 0), k, _on(ctx, out, x.dtype, "out", (T, H))))
+    T, H = shape = x.shape
+    k, rows, shared, dtype = topk_idx.shape[1], table.shape[0], 1 if has_shared else 0, x.dtype
+    st = lib().moe_expert_ffn_mx(ctx.handle, _dtype(x, "x"), _at(ctx, table, torch.int64, (rows, 6), "experts table"),
+                                 shared, _at(ctx, x, dtype, shape, "x"), _at(ctx, topk_idx, torch.int32, (T, k), "topk_idx"),
+                                 _at(ctx, topk_w, torch.float32, (T, k), "topk_w"), T, H, I, rows - shared, k,
+                                 _at(ctx, out, dtype, shape, "out"))
+    if st:
+        _ck(st)
     return out
 
 

@@ -75,16 +75,25 @@ hipEvent_t moe_timing_event(moe_ctx *ctx);
 // carries the start/stop events (hipExtLaunchKernelGGL), so the recorded time
 // is the kernel's own execution, not that of extra event packets around it.
 template <typename K, typename... Args>
-void moe_launch_on(moe_ctx *ctx, hipStream_t stream, int stage, K kernel, dim3 grid, dim3 block, Args... args) {
+void moe_launch_all(moe_ctx *ctx, hipStream_t stream, int stage, K kernel, dim3 grid, dim3 block, size_t lds, Args... args) {
   hipEvent_t s = ctx->timing ? moe_timing_event(ctx) : nullptr;
   hipEvent_t e = s ? moe_timing_event(ctx) : nullptr;
   if (s && e) {
-    hipExtLaunchKernelGGL(kernel, grid, block, 0, stream, s, e, 0, args...);
+    hipExtLaunchKernelGGL(kernel, grid, block, lds, stream, s, e, 0, args...);
     ctx->timed.push_back({s, e, stage});
     return;
   }
   if (s) ctx->event_pool.push_back(s);
-  hipLaunchKernelGGL(kernel, grid, block, 0, stream, args...);
+  hipLaunchKernelGGL(kernel, grid, block, lds, stream, args...);
+}
+template <typename K, typename... Args>
+void moe_launch_on(moe_ctx *ctx, hipStream_t stream, int stage, K kernel, dim3 grid, dim3 block, Args... args) {
+  moe_launch_all(ctx, stream, stage, kernel, grid, block, 0, args...);
+}
+// With `lds` bytes of dynamic LDS.
+template <typename K, typename... Args>
+void moe_launch_lds(moe_ctx *ctx, int stage, K kernel, dim3 grid, dim3 block, size_t lds, Args... args) {
+  moe_launch_all(ctx, ctx->stream, stage, kernel, grid, block, lds, args...);
 }
 template <typename K, typename... Args>
 void moe_launch(moe_ctx *ctx, int stage, K kernel, dim3 grid, dim3 block, Args... args) {

@@ -151,8 +151,8 @@ extern "C" moe_status moe_expert_ffn_mx(moe_ctx *ctx, int dtype, const moe_mx_ex
   if ((st = moe_scratch(ctx, l.size, &scr))) return st;
   uint8_t *b = static_cast<uint8_t *>(scr);
   int32_t *offsets = reinterpret_cast<int32_t *>(b + o_offsets), *perm = reinterpret_cast<int32_t *>(b + o_perm);
-  if ((st = launch_mx_quantize(ctx, dtype, x, T, H, H, b + o_x, b + o_sx))) return st;
-  if ((st = launch_bucket_public(ctx, topk_idx, T, k, E, reinterpret_cast<int32_t *>(b + o_counts), offsets, perm)))
+  if ((st = launch_mx_prep(ctx, dtype, x, T, H, b + o_x, b + o_sx, topk_idx, k, E, reinterpret_cast<int32_t *>(b + o_counts),
+                           offsets, perm)))
     return st;
   MxProduct p{};
   p.x = b + o_x, p.sx = b + o_sx, p.X = T, p.table = experts, p.N = I, p.K = H, p.E = E, p.L = routed, p.k = k;

@@ -38,6 +38,9 @@ moe_status launch_mx_quantize(moe_ctx *ctx, int dtype, const void *x, int64_t ro
                               uint8_t *codes, uint8_t *scales);
 moe_status launch_mx_dequantize(moe_ctx *ctx, int dtype, const uint8_t *codes, const uint8_t *scales, int64_t rows,
                                 int K, void *out);
+// Tokens' rows in 4 bits and, by expert, their entries t * k + j.
+moe_status launch_mx_prep(moe_ctx *ctx, int dtype, const void *x, int T, int H, uint8_t *codes, uint8_t *scales,
+                          const int32_t *idx, int k, int E, int32_t *counts, int32_t *offsets, int32_t *perm);
 // Whether a product goes to the tile kernels.
 bool mx_tiles(const moe_ctx *ctx, const MxProduct &p);
 // out = x w^T line by line

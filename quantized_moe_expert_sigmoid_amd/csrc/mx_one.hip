@@ -265,16 +265,7 @@ void gateup(moe_ctx *ctx, const MxOne &p) {
 
 template <bool WIDE, int STAGES, int DTYPE>
 void down(moe_ctx *ctx, const MxOne &p, int waves, size_t lds) {
-  hipEvent_t s = ctx->timing ? moe_timing_event(ctx) : nullptr, e = s ? moe_timing_event(ctx) : nullptr;
-  auto kernel = mx_one_down_kernel<WIDE, STAGES, DTYPE>;
-  const dim3 grid(p.H / 32, p.T), block(waves * 64);
-  if (s && e) {
-    hipExtLaunchKernelGGL(kernel, grid, block, lds, ctx->stream, s, e, 0, p);
-    ctx->timed.push_back({s, e, MOE_STAGE_DOWN});
-    return;
-  }
-  if (s) ctx->event_pool.push_back(s);
-  hipLaunchKernelGGL(kernel, grid, block, lds, ctx->stream, p);
+  moe_launch_lds(ctx, MOE_STAGE_DOWN, mx_one_down_kernel<WIDE, STAGES, DTYPE>, dim3(p.H / 32, p.T), dim3(waves * 64), lds, p);
 }
 
 template <bool WIDE, int DTYPE>

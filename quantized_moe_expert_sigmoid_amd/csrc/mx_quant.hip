@@ -62,6 +62,77 @@ moe_status dequantize(moe_ctx *ctx, const uint8_t *codes, const uint8_t *scales,
   return MOE_OK;
 }
 
+// Lines by expert and the tokens' rows in 4 bits, in one launch: workgroup 0 buckets the (token, slot) entries (an id of -1
+// gets none; one that is no expert, or that an earlier slot of the token has, gets none and is reported), the others
+// quantise. Entries of an expert are in no particular order: a line's result does not depend on its place.
+constexpr int kPrepEntries = 32768;  // 128 KB of LDS
+
+template <int DTYPE>
+__global__ __launch_bounds__(1024) void mx_prep_kernel(const void *x, int64_t n, uint32_t *codes, uint8_t *scales,
+                                                       const int32_t *idx, int entries, int k, int E, int32_t *offsets,
+                                                       int32_t *perm, uint32_t *err) {
+  extern __shared__ uint16_t ids[];  // [entries], then the entries in their order (stored one by one they took 10 us)
+  uint16_t *order = ids + entries;
+  __shared__ int count[1024], sums[16];
+  const int tid = threadIdx.x;
+  if (blockIdx.x) {
+    const int64_t i = (int64_t)(blockIdx.x - 1) * 1024 + tid;
+    if (i >= n) return;
+    float v[8];
+    mx_load8<DTYPE>(static_cast<const typename MxOut<DTYPE>::T *>(x) + i * 8, v);
+    uint32_t byte;
+    codes[i] = mx_codes8(v, byte);
+    if ((tid & 3) == 0) scales[i >> 2] = (uint8_t)byte;
+    return;
+  }
+  const int lane = tid & 63, wave = tid >> 6;
+  count[tid] = 0;
+  __syncthreads();
+  for (int t = tid; t * k < entries; t += 1024) {  // a thread has a token's ids at once
+    int id[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) id[j] = j < k ? idx[t * k + j] : -1;
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      bool ok = id[j] >= 0 && id[j] < E;
+#pragma unroll
+      for (int i = 0; i < j; ++i) ok &= id[i] != id[j];
+      bad |= !ok && id[j] != -1;
+      if (j < k) ids[t * k + j] = ok ? (uint16_t)id[j] : (uint16_t)0xffff;
+      if (ok) atomicAdd(&count[id[j]], 1);
+    }
+    if (bad) atomicOr(err, (uint32_t)ERRF_BAD_INDEX);
+  }
+  __syncthreads();
+  const int c = count[tid], sum = mx_scan(c);
+  if (lane == 63) sums[wave] = sum;
+  __syncthreads();
+  int at = sum - c;
+  for (int w = 0; w < wave; ++w) at += sums[w];
+  if (tid < E) offsets[tid] = at;
+  if (tid == E - 1) offsets[E] = at + c;
+  count[tid] = at;
+  __syncthreads();
+  for (int i = tid; i < entries; i += 1024)
+    if (ids[i] != 0xffff) order[atomicAdd(&count[ids[i]], 1)] = (uint16_t)i;
+  __syncthreads();
+  int all = 0;
+  for (int w = 0; w < 16; ++w) all += sums[w];
+  for (int i = tid; i < all; i += 1024) perm[i] = order[i];
+}
+
+template <int DTYPE>
+moe_status prep(moe_ctx *ctx, const void *x, int T, int H, uint8_t *codes, uint8_t *scales, const int32_t *idx, int k, int E,
+                int32_t *offsets, int32_t *perm) {
+  const int64_t n = (int64_t)T * (H / 8);
+  moe_launch_lds(ctx, MOE_STAGE_BUCKET, mx_prep_kernel<DTYPE>, dim3((unsigned)((n + 1023) / 1024 + 1)), dim3(1024),
+                 (size_t)T * k * 4, x, n, reinterpret_cast<uint32_t *>(codes), scales, idx, T * k, k, E, offsets, perm,
+                 ctx->dev_small);
+  MOE_CHECK_LAUNCH("mx_prep_kernel");
+  return MOE_OK;
+}
+
 // out[t] = y_shared[t] + sum_j w[t][j] y[t][j], fused multiply-adds in fp32 in slot order, rounded once. Slots of zero
 // weight and slots whose id is no expert, or one that an earlier slot of the token has, are left out unread. y: the
 // T * k slots in order, then the shared expert's T rows. A workgroup's threads have one token, so that ids and weights
@@ -70,17 +141,19 @@ template <int Y, int DTYPE>
 __global__ __launch_bounds__(256) void mx_combine_kernel(const typename MxOut<Y>::T *y, const int32_t *idx,
                                                          const float *w, int T, int k, int E, int H, int has_shared,
                                                          typename MxOut<DTYPE>::T *out) {
-  typedef typename MxOut<Y>::V V;
   constexpr int kMaxK = 16;
-  const int per = (H / 4 + 255) / 256;
+  struct V8 {
+    typename MxOut<Y>::V a, b;
+  };
+  const int per = (H / 8 + 255) / 256;
   const int64_t t = blockIdx.x / per;
-  const int h = (int)(blockIdx.x % per * 256 + threadIdx.x) * 4;
+  const int h = (int)(blockIdx.x % per * 256 + threadIdx.x) * 8;
   if (h >= H) return;
   bool used[kMaxK];
   int id[kMaxK];
   float f[kMaxK];
-  V v[kMaxK], sh = {};
-  if (has_shared) sh = *reinterpret_cast<const V *>(y + (T * (int64_t)k + t) * H + h);
+  V8 v[kMaxK], sh = {};
+  if (has_shared) sh = *reinterpret_cast<const V8 *>(y + (T * (int64_t)k + t) * H + h);
 #pragma unroll
   for (int j = 0; j < kMaxK; ++j) {
     id[j] = idx[t * k + min(j, k - 1)];
@@ -91,16 +164,22 @@ __global__ __launch_bounds__(256) void mx_combine_kernel(const typename MxOut<Y>
     used[j] = j < k && f[j] != 0.0f && id[j] >= 0 && id[j] < E;
 #pragma unroll
     for (int i = 0; i < j; ++i) used[j] &= id[i] != id[j];
-    if (used[j]) v[j] = *reinterpret_cast<const V *>(y + (t * k + j) * H + h);
+    if (used[j]) v[j] = *reinterpret_cast<const V8 *>(y + (t * k + j) * H + h);
   }
-  f32x4 acc = {(float)sh[0], (float)sh[1], (float)sh[2], (float)sh[3]};
+  f32x4 a = {(float)sh.a[0], (float)sh.a[1], (float)sh.a[2], (float)sh.a[3]};
+  f32x4 b = {(float)sh.b[0], (float)sh.b[1], (float)sh.b[2], (float)sh.b[3]};
 #pragma unroll
   for (int j = 0; j < kMaxK; ++j)
     if (used[j]) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(f[j], (float)v[j][c], acc[c]);
+      for (int c = 0; c < 4; ++c) {
+        a[c] = __builtin_fmaf(f[j], (float)v[j].a[c], a[c]);
+        b[c] = __builtin_fmaf(f[j], (float)v[j].b[c], b[c]);
+      }
     }
-  *reinterpret_cast<typename MxOut<DTYPE>::V *>(out + t * H + h) = MxOut<DTYPE>::of(acc);
+  typename MxOut<DTYPE>::V *o = reinterpret_cast<typename MxOut<DTYPE>::V *>(out + t * H + h);
+  o[0] = MxOut<DTYPE>::of(a);
+  o[1] = MxOut<DTYPE>::of(b);
 }
 
 template <int Y, int DTYPE>
@@ -109,7 +188,7 @@ void combine(moe_ctx *ctx, const void *y, const int32_t *idx, const float *w, in
   typedef typename MxOut<Y>::T TY;
   typedef typename MxOut<DTYPE>::T TO;
   moe_launch(ctx, MOE_STAGE_COMBINE, mx_combine_kernel<Y, DTYPE>,
-             dim3((unsigned)(T * ((H / 4 + 255) / 256))), dim3(256), static_cast<const TY *>(y), idx, w, T, k,
+             dim3((unsigned)(T * ((H / 8 + 255) / 256))), dim3(256), static_cast<const TY *>(y), idx, w, T, k,
              E, H, has_shared, static_cast<TO *>(out));
 }
 
@@ -130,6 +209,19 @@ moe_status launch_mx_dequantize(moe_ctx *ctx, int dtype, const uint8_t *codes, c
     case MOE_FP32: return dequantize<MOE_FP32>(ctx, codes, scales, rows, K, out);
     case MOE_BF16: return dequantize<MOE_BF16>(ctx, codes, scales, rows, K, out);
     default: return dequantize<MOE_FP16>(ctx, codes, scales, rows, K, out);
+  }
+}
+
+moe_status launch_mx_prep(moe_ctx *ctx, int dtype, const void *x, int T, int H, uint8_t *codes, uint8_t *scales,
+                          const int32_t *idx, int k, int E, int32_t *counts, int32_t *offsets, int32_t *perm) {
+  if ((int64_t)T * k > kPrepEntries) {  // more than one workgroup buckets well
+    moe_status st = launch_mx_quantize(ctx, dtype, x, T, H, H, codes, scales);
+    return st ? st : launch_bucket_public(ctx, idx, T, k, E, counts, offsets, perm);
+  }
+  switch (dtype) {
+    case MOE_FP32: return prep<MOE_FP32>(ctx, x, T, H, codes, scales, idx, k, E, offsets, perm);
+    case MOE_BF16: return prep<MOE_BF16>(ctx, x, T, H, codes, scales, idx, k, E, offsets, perm);
+    default: return prep<MOE_FP16>(ctx, x, T, H, codes, scales, idx, k, E, offsets, perm);
   }
 }
 

@@ -283,7 +283,9 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
       }
     }
   } else {
-    const bool vec = p.N % 4 == 0;
+    // 16 bytes a store: four fp32 values; of 16-bit ones two groups of four, of which the halves of a wave (one line's, both
+    // here or neither) trade one each. Rows that do not end on 16 bytes: one value a store.
+    const bool vec = p.N % (DTYPE == MOE_FP32 ? 4 : 8) == 0;
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
       const int m = row_x[j] + l32;
@@ -295,20 +297,34 @@ __global__ __launch_bounds__(WM *WN * 64, OCC) void mx_tile_kernel(MxProduct p, 
       if (r < 0) continue;
       typename O::T *out = static_cast<typename O::T *>(p.out) + r * p.N;
 #pragma unroll
-      for (int i = 0; i < FN; ++i)
+      for (int i = 0; i < FN; ++i) {
+        const f32x16 &c = acc[i][j];
+        const int n = n0 + row_w[i] - BM;
+        if (vec && DTYPE != MOE_FP32) {
+#pragma unroll
+          for (int g = 0; g < 4; g += 2) {
+            const uint2 a = __builtin_bit_cast(uint2, MxOut<DTYPE == MOE_FP32 ? MOE_BF16 : DTYPE>::of(f32x4{c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]}));
+            const uint2 b = __builtin_bit_cast(uint2, MxOut<DTYPE == MOE_FP32 ? MOE_BF16 : DTYPE>::of(f32x4{c[4 * g + 4], c[4 * g + 5], c[4 * g + 6], c[4 * g + 7]}));
+            const auto x = __builtin_amdgcn_permlane32_swap(a.x, b.x, false, false);
+            const auto y = __builtin_amdgcn_permlane32_swap(a.y, b.y, false, false);
+            const uint4 v = {x[0], y[0], x[1], y[1]};
+            if (n + 8 * (g + hl) < p.N) *reinterpret_cast<uint4 *>(out + n + 8 * (g + hl)) = v;
+          }
+          continue;
+        }
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int n = n0 + row_w[i] - BM + 8 * g + 4 * hl;
-          const f32x16 &c = acc[i][j];
+          const int at = n + 8 * g + 4 * hl;
           const f32x4 v = {c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]};
           if (vec) {
-            if (n < p.N) *reinterpret_cast<typename O::V *>(out + n) = O::of(v);
+            if (at < p.N) *reinterpret_cast<typename O::V *>(out + at) = O::of(v);
           } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (n + e < p.N) out[n + e] = O::one(v[e]);
+              if (at + e < p.N) out[at + e] = O::one(v[e]);
           }
         }
+      }
     }
   }
 }

@@ -485,3 +485,20 @@ def test_refusals(moe, ctx):
             call()
     assert ffn(f(0, 64), i32(0, 2), f(0, 2), 64, f(0, 64)).shape == (0, 64)
     ctx.check()
+
+
+@pytest.mark.parametrize("T,k,E", [(4097, 8, 9), (2050, 16, 300), (1000, 5, 1024), (64, 7, 7)])
+def test_ffn_bucketing(moe, ctx, T, k, E):
+    """Many entries (one workgroup's and more than that), odd numbers of slots, dropped ones among them."""
+    H, I = 64, 64
+    rng = np.random.default_rng(k)
+    experts = Experts(moe, ctx, 5, E, H, I)
+    x = torch.from_numpy(rng.standard_normal((T, H))).to(BF16).cuda()
+    idx = np.argsort(rng.random((T, E)), axis=1)[:, :k].astype(np.int32)
+    idx[rng.random((T, k)) < 0.1] = -1
+    w = np.where(idx < 0, 0, rng.random((T, k))).astype(np.float32)
+    out = torch.empty_like(x)
+    moe.moe_expert_ffn_mx(ctx, experts.blocks.table, False, x, torch.from_numpy(idx).cuda(), torch.from_numpy(w).cuda(), I,
+                          out)
+    ctx.check()
+    check_ffn(out, x, idx, w, experts, E, False)

@@ -235,57 +235,66 @@ __device__ __forceinline__ int mx_scan(int v) {
   return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
 }
 
-// Unit u of the lines in tiles: the shared expert's tiles first, then each
+// The lines in tiles: units are the shared expert's tiles first, then each
 // expert's, in order. Every wave finds its unit by itself, in one round trip
 // to memory: a lane counts the tiles of E / 64 experts in a row (at most 16), a
 // scan over the wave's lanes and a ballot name the lane. Offsets that do not
 // ascend within 0 .. L are reported and cut to that range.
 template <int TILE>
-__device__ __forceinline__ MxUnit mx_unit(const MxProduct &p, int64_t u) {
-  const int64_t s = (p.shared + TILE - 1) / TILE;
-  if (u < s) return MxUnit{p.E, p.L + u * TILE, (int)min((int64_t)TILE, p.shared - u * TILE)};
-  u -= s;
-  if (!p.offsets) {
-    const int64_t left = p.L - u * TILE;
-    return MxUnit{0, u * TILE, (int)max((int64_t)0, min((int64_t)TILE, left))};
-  }
-  const int lane = (int)(threadIdx.x & 63), per = (p.E + 63) / 64, e0 = lane * per;
-  const int top = (int)p.L;
+struct MxUnits {
   int v[17];  // offsets of this lane's experts, the next lane's first one last
+  int tiles, sum, per;
+
+  __device__ __forceinline__ bool used(int i) const { return i <= 4 || (i + 3) / 4 * 4 - 4 < per; }  // all lanes alike
+  __device__ __forceinline__ void load(const MxProduct &p) {
+    if (!p.offsets) return;
+    const int lane = (int)(threadIdx.x & 63), top = (int)p.L;
+    per = (p.E + 63) / 64;
+    const int e0 = lane * per;
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-    if (c == 0 || 4 * c < per) {  // all lanes alike
-      if (c == 0) v[0] = p.offsets[min(e0, p.E)];
+    for (int c = 0; c < 4; ++c)
+      if (used(4 * c + 1)) {
+        if (c == 0) v[0] = p.offsets[min(e0, p.E)];
 #pragma unroll
-      for (int i = 1; i <= 4; ++i) v[4 * c + i] = p.offsets[min(e0 + min(4 * c + i, per), p.E)];
+        for (int i = 1; i <= 4; ++i) v[4 * c + i] = p.offsets[min(e0 + min(4 * c + i, per), p.E)];
+      }
+    bool ok = v[0] >= 0 && v[0] <= top;
+    v[0] = min(max(v[0], 0), top);
+    tiles = 0;
+#pragma unroll
+    for (int i = 1; i <= 16; ++i)
+      if (used(i)) {
+        ok &= v[i] >= v[i - 1] && v[i] <= top;
+        v[i] = max(v[i - 1], min(v[i], top));
+        tiles += (v[i] - v[i - 1] + TILE - 1) / TILE;
+      }
+    if (!ok) atomicOr(p.err, (uint32_t)ERRF_MX);
+    sum = mx_scan(tiles);
+  }
+  __device__ __forceinline__ MxUnit find(const MxProduct &p, int64_t u) const {
+    const int64_t s = (p.shared + TILE - 1) / TILE;
+    if (u < s) return MxUnit{p.E, p.L + u * TILE, (int)min((int64_t)TILE, p.shared - u * TILE)};
+    u -= s;
+    if (!p.offsets) {
+      const int64_t left = p.L - u * TILE;
+      return MxUnit{0, u * TILE, (int)max((int64_t)0, min((int64_t)TILE, left))};
     }
-  bool ok = v[0] >= 0 && v[0] <= top;
-  v[0] = min(max(v[0], 0), top);
-  int tiles = 0;
+    const uint64_t past = __ballot((int64_t)sum > u);
+    if (!past) return MxUnit{0, 0, 0};
+    const int who = __ffsll((unsigned long long)past) - 1;
+    int left = (int)u - __builtin_amdgcn_readlane(sum - tiles, who), lo = __builtin_amdgcn_readlane(v[0], who);
+    MxUnit r{0, 0, 0};
 #pragma unroll
-  for (int i = 1; i <= 16; ++i)
-    if (i <= 4 || (i + 3) / 4 * 4 - 4 < per) {
-      ok &= v[i] >= v[i - 1] && v[i] <= top;
-      v[i] = max(v[i - 1], min(v[i], top));
-      tiles += (v[i] - v[i - 1] + TILE - 1) / TILE;
-    }
-  if (!ok) atomicOr(p.err, (uint32_t)ERRF_MX);
-  const int sum = mx_scan(tiles);
-  const uint64_t past = __ballot((int64_t)sum > u);
-  if (!past) return MxUnit{0, 0, 0};
-  const int who = __ffsll((unsigned long long)past) - 1;
-  int left = (int)u - __builtin_amdgcn_readlane(sum - tiles, who), lo = __builtin_amdgcn_readlane(v[0], who);
-  MxUnit r{0, 0, 0};
-#pragma unroll
-  for (int i = 1; i <= 16; ++i)
-    if ((i <= 4 || (i + 3) / 4 * 4 - 4 < per) && r.n == 0) {
-      const int hi = __builtin_amdgcn_readlane(v[i], who), n = (hi - lo + TILE - 1) / TILE;
-      if (left < n) r = MxUnit{who * per + i - 1, lo + left * TILE, min(TILE, hi - lo - left * TILE)};
-      left -= n;
-      lo = hi;
-    }
-  return r;
-}
+    for (int i = 1; i <= 16; ++i)
+      if (used(i) && r.n == 0) {
+        const int hi = __builtin_amdgcn_readlane(v[i], who), n = (hi - lo + TILE - 1) / TILE;
+        if (left < n) r = MxUnit{who * per + i - 1, lo + left * TILE, min(TILE, hi - lo - left * TILE)};
+        left -= n;
+        lo = hi;
+      }
+    return r;
+  }
+};
 
 // Row of x of a line, and where its result goes; -1: out of range, which is reported.
 __device__ __forceinline__ int64_t mx_in_row(const MxProduct &p, int64_t line) {

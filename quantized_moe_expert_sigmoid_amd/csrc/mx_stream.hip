@@ -63,7 +63,9 @@ __global__ __launch_bounds__(kWaves * 64, 4) void mx_stream_kernel(MxProduct p) 
   typedef MxOut<DTYPE> O;
   __shared__ f32x4 box[kWaves * NM * 64];
   const int lane = threadIdx.x & 63, wave = mx_uniform((int)(threadIdx.x >> 6));
-  const MxUnit u = mx_unit<16 * NM>(p, blockIdx.y);
+  MxUnits<16 * NM> lines;
+  lines.load(p);
+  const MxUnit u = lines.find(p, blockIdx.y);
   if (u.n == 0) return;
   const int n0 = (int)blockIdx.x * 16;
   const int blocks = p.K / kMxBlock, steps = (blocks + 3) / 4, per = (steps + kWaves - 1) / kWaves;

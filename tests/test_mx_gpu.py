@@ -502,3 +502,100 @@ def test_ffn_bucketing(moe, ctx, T, k, E):
                           out)
     ctx.check()
     check_ffn(out, x, idx, w, experts, E, False)
+
+
+# --- more tiles than workgroups ---------------------------------------------------
+
+@pytest.mark.parametrize("M,N,K,at", [(2100, 9000, 64, 0), (2100, 9000, 96, 1), (3, 50000, 128, 0), (20, 100000, 512, 0),
+                                      (700, 20000, 512, 0), (1000, 9100, 1056, 0)])
+def test_product_of_many_tiles(moe, ctx, M, N, K, at):
+    """Workgroups take several tiles each, of few stages and of more."""
+    rng = np.random.default_rng(M + K)
+    x, w = ref.random_matrix(rng, M, K), ref.random_matrix(rng, N, K, lo=112, hi=122)
+    sw = torch.empty(at + w[1].size, dtype=torch.uint8, device="cuda")[at:].view(N, -1)
+    sw.copy_(torch.from_numpy(w[1]))
+    out = torch.full((M + 1, N), 12345.0, device="cuda")
+    moe.moe_mx_matmul(ctx, *dev(x), torch.from_numpy(w[0]).cuda(), sw, out[:-1])
+    ref.check_product(out[:-1], ref.dequantize(*x), ref.dequantize(*w), (M, N, K))
+    assert (out[-1] == 12345.0).all()
+
+
+@pytest.mark.parametrize("E,N,K,most", [(300, 1100, 96, 9), (300, 600, 512, 40), (64, 2100, 64, 300), (40, 2100, 512, 900)])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_grouped_of_many_tiles(moe, ctx, E, N, K, most, dtype):
+    """Tiles without lines before, between and behind those that a workgroup computes; lines gathered and scattered."""
+    rng = np.random.default_rng(E + most)
+    counts = np.where(rng.random(E) < 0.4, 0, rng.integers(0, most, E))
+    counts[:E // 8] = 0
+    counts[-E // 8:] = 0
+    L = int(counts.sum())
+    x, w = ref.random_matrix(rng, 37, K), ref.random_matrix(rng, E, N, K, lo=112, hi=122)
+    grouped(moe, ctx, x, w, counts, dtype, rng.integers(0, 37, L), rng.permutation(L + 9)[:L], L + 9)
+
+
+@pytest.mark.parametrize("T,k,E,H,I", [(40, 8, 100, 64, 2048), (40, 8, 50, 512, 1024), (700, 4, 20, 192, 1600),
+                                       (900, 4, 12, 512, 2560)])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_ffn_of_many_tiles(moe, ctx, T, k, E, H, I, dtype):
+    rng = np.random.default_rng(T + E)
+    experts = Experts(moe, ctx, E, E + 1, H, I)
+    x = torch.from_numpy(rng.standard_normal((T, H))).to(dtype).cuda()
+    idx = np.argsort(rng.random((T, E)) + 0.02 * np.arange(E), axis=1)[:, :k].astype(np.int32)
+    w = rng.random((T, k)).astype(np.float32)
+    out = torch.full_like(x, 9.0)
+    moe.moe_expert_ffn_mx(ctx, experts.blocks.table, True, x, torch.from_numpy(idx).cuda(), torch.from_numpy(w).cuda(), I, out)
+    ctx.check()
+    check_ffn(out, x, idx, w, experts, E, True)
+
+
+# --- offsets beyond 32 bits ---------------------------------------------------------
+
+def test_quantize_far(moe, ctx):
+    """More than 2^31 values and 2^32 bytes, there and back, and a row stride that passes 2^32 bytes within a few rows."""
+    rows, K = (1 << 21) + 5, 1056
+    x = torch.empty((rows, K), device="cuda").normal_()
+    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((rows, K // 32), dtype=torch.uint8, device="cuda")
+    moe.moe_mx_quantize(ctx, x, codes, scales)
+    out = torch.empty((rows, K), dtype=BF16, device="cuda")
+    moe.moe_mx_dequantize(ctx, codes, scales, out)
+    for r in (0, (1 << 29) // K, (1 << 30) // K, (1 << 31) // K, rows - 3):
+        part = slice(r, r + 3)
+        check_quantized((codes[part].cpu().numpy(), scales[part].cpu().numpy()), x[part])
+        want = ref.dequantize(codes[part].cpu().numpy(), scales[part].cpu().numpy())
+        assert np.array_equal(out[part].double().cpu().numpy(), want)  # 4 bits' values are bf16's too
+    del x, out
+    y = torch.empty((50, 1 << 26), dtype=BF16, device="cuda")[:, 64:160]
+    y.copy_(torch.randn((50, 96), generator=torch.Generator().manual_seed(2)))
+    check_quantized(quantize(moe, ctx, y), y)
+
+
+def test_grouped_far(moe, ctx):
+    """Rows of x, weights and out beyond 2^32 bytes."""
+    E, N, K, X, R = 600, 2048, 8192, 1_100_000, 600_000
+    rand = lambda lo, hi, *s: torch.randint(lo, hi, s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    w, sw = rand(0, 256, E, N, K // 2), rand(112, 122, E, N, K // 32)
+    x, sx = rand(0, 256, X, K // 2), rand(118, 130, X, K // 32)
+    assert min(w.numel(), x.numel(), R * N * 4) > 1 << 32
+    i32 = lambda v: torch.from_numpy(np.asarray(v, dtype=np.int32)).cuda()  # noqa: E731
+    rng = np.random.default_rng(0)
+    for lines in ((0, 0, 1), (1, 20, 7), (60, 0, 300)):
+        counts = np.zeros(E, dtype=np.int64)
+        counts[[0, E - 2, E - 1]] = lines
+        L = int(counts.sum())
+        in_rows, out_rows = X - 1 - rng.permutation(1000)[:L], R - 1 - rng.permutation(1000)[:L]
+        in_rows[0], out_rows[-1] = X - 1, R - 1
+        out_rows[:-1] = R - 2 - rng.permutation(1000)[:L - 1]
+        out = torch.full((R, N), 12345.0, device="cuda")
+        moe.moe_mx_grouped_matmul(ctx, x, sx, w, sw, i32(np.concatenate([[0], np.cumsum(counts)])), out, in_rows=i32(in_rows),
+                                  out_rows=i32(out_rows))
+        ctx.check()
+        first = 0
+        for e in np.flatnonzero(counts):
+            l = slice(first, first + int(counts[e]))
+            src, dst = torch.from_numpy(in_rows[l]).cuda(), torch.from_numpy(out_rows[l]).cuda()
+            ref.check_product(out[dst], ref.dequantize(x[src].cpu().numpy(), sx[src].cpu().numpy()),
+                              ref.dequantize(w[e].cpu().numpy(), sw[e].cpu().numpy()), (lines, e))
+            out[dst] = 12345.0
+            first = l.stop
+        assert (out == 12345.0).all()

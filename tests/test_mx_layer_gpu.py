@@ -85,10 +85,10 @@ def test_steps_make_the_ffn(moe, ctx):
         check_ffn(got, x, idx.cpu().numpy(), w.cpu().numpy(), experts, E, False)
 
 
-@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("T", [1, 2, 40])
 def test_ffn_graph(moe, T):
     """A captured call replayed on other tokens and routing, eager work between."""
-    E, k, H, I = 8, 2, 192, 128
+    E, k, H, I = 16, 2, 192, 128
     stream = torch.cuda.Stream()
     c = moe.MoeCtx(0, stream)
     rng = np.random.default_rng(T)
@@ -146,3 +146,59 @@ def test_two_contexts_on_two_streams(moe):
     finally:
         for c in ctxs:
             c.close()
+
+
+@pytest.mark.parametrize("T", [1, 3, 50])
+def test_ffn_timing(moe, T):
+    """With per-kernel timing on results are the same, and every launch is counted."""
+    E, k, H, I = 24, 2, 128, 192
+    c = moe.MoeCtx(0)
+    try:
+        experts = Experts(moe, c, 3, E + 1, H, I)
+        rng = np.random.default_rng(T)
+        x = torch.from_numpy(rng.standard_normal((T, H))).to(BF16).cuda()
+        idx = torch.from_numpy(np.argsort(rng.random((T, E)), axis=1)[:, :k].astype(np.int32)).cuda()
+        w = torch.from_numpy(rng.random((T, k)).astype(np.float32)).cuda()
+        plain, timed = torch.empty_like(x), torch.empty_like(x)
+        moe.moe_expert_ffn_mx(c, experts.blocks.table, True, x, idx, w, I, plain)
+        c.enable_timing(True)
+        for _ in range(3):
+            moe.moe_expert_ffn_mx(c, experts.blocks.table, True, x, idx, w, I, timed)
+        times = c.read_timing()
+        c.enable_timing(False)
+        assert torch.equal(plain, timed)
+        for stage in ("gateup", "down") + (("bucket", "combine") if T > 3 else ()):
+            assert times[stage][1] == 3 and times[stage][0] > 0, times
+    finally:
+        c.close()
+
+
+def test_experts_gigabytes_apart(moe):
+    """The table's pointers may lie anywhere: one expert's block far from the others'."""
+    E, k, H, I, T = 3, 2, 256, 128, 20
+    c = moe.MoeCtx(0)
+    try:
+        experts = Experts(moe, c, 4, E, H, I)
+        far = torch.empty(5 << 30, dtype=torch.uint8, device="cuda")
+        table = experts.blocks.table.clone()
+        old = table[1].cpu()
+        start = int(old.min())
+        at = (far.data_ptr() + far.numel() - 2 * experts.blocks.block_bytes) // 256 * 256
+        views = experts.blocks.views(1)
+        offsets = [int(v) - start for v in old]
+        base = at - far.data_ptr()
+        for v, o in zip(views, offsets):
+            far[base + o:base + o + v.numel()].copy_(v.reshape(-1))
+        table[1] = torch.tensor([at + o for o in offsets])
+        rng = np.random.default_rng(1)
+        x = torch.from_numpy(rng.standard_normal((T, H))).to(BF16).cuda()
+        idx = np.argsort(rng.random((T, E)), axis=1)[:, :k].astype(np.int32)
+        w = rng.random((T, k)).astype(np.float32)
+        for n in (1, T):
+            out = torch.empty_like(x[:n])
+            moe.moe_expert_ffn_mx(c, table, False, x[:n], torch.from_numpy(idx[:n]).cuda(), torch.from_numpy(w[:n]).cuda(), I,
+                                  out)
+            check_ffn(out, x[:n], idx[:n], w[:n], experts, E, False)
+        c.check()
+    finally:
+        c.close()

@@ -599,3 +599,39 @@ def test_grouped_far(moe, ctx):
             out[dst] = 12345.0
             first = l.stop
         assert (out == 12345.0).all()
+
+
+# --- ends of the ranges, NaN where nothing may come from it ------------------------------
+
+@pytest.mark.parametrize("M,N", [(2, 70), (70, 130), (300, 257)])
+def test_product_of_longest_rows(moe, ctx, M, N):
+    rng = np.random.default_rng(M)
+    x, w = ref.random_matrix(rng, M, 65536), ref.random_matrix(rng, N, 65536, lo=112, hi=122)
+    ref.check_product(product(moe, ctx, x, w, FP32), ref.dequantize(*x), ref.dequantize(*w), (M, N))
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 40])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_ffn_of_bad_token_and_unused_bad_expert(moe, ctx, T, bad):
+    """A token that holds NaN or an infinity gets NaN, others what they get without it; an expert of NaN that has
+    weight 0 adds nothing."""
+    E, k, H, I = 40, 3, 192, 128
+    experts = Experts(moe, ctx, 11, E + 1, H, I)
+    rng = np.random.default_rng(T)
+    x = torch.from_numpy(rng.standard_normal((T, H))).to(BF16).cuda()
+    idx = np.argsort(rng.random((T, E - 1)), axis=1)[:, :k].astype(np.int32)
+    idx[:, 1] = E - 1
+    w = rng.random((T, k)).astype(np.float32)
+    w[:, 1] = 0
+    for v in experts.blocks.views(E - 1)[3:]:
+        v.fill_(255)
+    args = (torch.from_numpy(idx).cuda(), torch.from_numpy(w).cuda(), I)
+    out = torch.empty_like(x)
+    moe.moe_expert_ffn_mx(ctx, experts.blocks.table, True, x, *args, out)
+    ctx.check()
+    check_ffn(out, x, np.where(idx == E - 1, -1, idx), w, experts, E, True)
+    spoiled, y = torch.empty_like(x), x.clone()
+    y[T - 1, H - 1] = bad
+    moe.moe_expert_ffn_mx(ctx, experts.blocks.table, True, y, *args, spoiled)
+    assert spoiled[T - 1].isnan().all()
+    assert torch.equal(spoiled[:T - 1], out[:T - 1])

@@ -9,6 +9,8 @@
 // Bound by the bytes. A thread has 8 values of a block (16 bytes of a 16-bit
 // type, 32 of fp32), four neighbouring lanes share a block's maximum by DPP, and
 // a thread stores its 8 codes as one word.
+// 2047 rows of 6144 bf16: 7.5 us, and 7.1 us back; 32768 rows of 6144 fp32 (912 MB):
+// 194 us (4.7 TB/s) and 181 us back (5.0), a copy's rate here being 5.1.
 #include "mx.h"
 
 namespace {
@@ -64,7 +66,8 @@ moe_status dequantize(moe_ctx *ctx, const uint8_t *codes, const uint8_t *scales,
 
 // Lines by expert and the tokens' rows in 4 bits, in one launch: workgroup 0 buckets the (token, slot) entries (an id of -1
 // gets none; one that is no expert, or that an earlier slot of the token has, gets none and is reported), the others
-// quantise. Entries of an expert are in no particular order: a line's result does not depend on its place.
+// quantise. Entries of an expert are in no particular order: a line's result does not depend on its place. 64 tokens of 8
+// experts: 6 us, 2048: 17 to 21 (two launches: 13 us more with 64 tokens).
 constexpr int kPrepEntries = 32768;  // 128 KB of LDS
 
 template <int DTYPE>
@@ -136,7 +139,8 @@ moe_status prep(moe_ctx *ctx, const void *x, int T, int H, uint8_t *codes, uint8
 // out[t] = y_shared[t] + sum_j w[t][j] y[t][j], fused multiply-adds in fp32 in slot order, rounded once. Slots of zero
 // weight and slots whose id is no expert, or one that an earlier slot of the token has, are left out unread. y: the
 // T * k slots in order, then the shared expert's T rows. A workgroup's threads have one token, so that ids and weights
-// are scalars; every slot's values are loaded before the first is used.
+// are scalars; every slot's values are loaded before the first is used. 2048 tokens of 8 bf16 slots and the shared
+// expert's, hidden 6144 (251 MB): 42 to 49 us, 5.2 TB/s at best; 64 tokens of fp32 slots 5.7 us.
 template <int Y, int DTYPE>
 __global__ __launch_bounds__(256) void mx_combine_kernel(const typename MxOut<Y>::T *y, const int32_t *idx,
                                                          const float *w, int T, int k, int E, int H, int has_shared,

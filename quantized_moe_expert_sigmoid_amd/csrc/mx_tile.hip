@@ -17,6 +17,11 @@
 // A wave has the operands of the next product step in registers before the
 // present one begins, and a stage's place is loaded again while its last products
 // run: STAGES - 1 stages are in flight.
+//
+// 2048 lines, 24576 rows of 6144: 185 us, 3.34 PFLOP/s (without the products 146,
+// without the loads 138: the loads bound it, at the rate at which they write LDS).
+// 2047 tokens of 8 of 256 experts of 4096 rows of 6144: 768 us, without the products
+// 758: the weights' bytes.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

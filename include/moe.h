@@ -649,9 +649,9 @@ size_t moe_mx_expert_layout(int H, int I, size_t *offsets_host);
  *   out[t] = FFN_E(t) (with has_shared) + sum_j topk_w[t][j] FFN_e(t), e =
  *   topk_idx[t][j];  FFN(t) = down q(silu(gate q(x[t])) * (up q(x[t]))),
  * q: to 4 bits as moe_mx_quantize does it. silu(g) = g / (1 + exp(-g)) in fp32 as
- * in moe_expert_ffn_q4; the slots' results are fp32 (MOE_BF16: rounded to bf16
- * where a call of several tokens stores them) and summed in fp32, the shared
- * expert's first, then in slot order.
+ * in moe_expert_ffn_q4; the slots' results are fp32 whatever the type and the
+ * number of tokens, and summed in fp32, the shared expert's first, then in slot
+ * order; the sum alone is rounded.
  * experts: DEVICE array [E], or [E + 1] with has_shared, whose last entry is the
  * shared expert. x and out (not the same array) are of type dtype. topk_idx int32
  * and topk_w fp32 [T][k] as moe_router_topk gives them. Slots of weight 0 or id

@@ -131,9 +131,6 @@ extern "C" moe_status moe_expert_ffn_mx(moe_ctx *ctx, int dtype, const moe_mx_ex
   REQUIRE(experts && x && topk_idx && topk_w && out, "%s: NULL pointer", fn);
   REQUIRE(moe_aligned16(x) && moe_aligned16(out), "%s: x and out must be 16-byte aligned", fn);
   REQUIRE(x != out, "%s: out must not be x", fn);
-  // the slots' results: bf16 ones are rounded to bf16 before they are summed (a quarter of a call of 2048 tokens' bytes
-  // beside the weights is theirs); fp16 ones are not, since a slot may pass fp16's range where the sum does not
-  const int y_dtype = dtype == MOE_BF16 ? MOE_BF16 : MOE_FP32;
   const int64_t routed = (int64_t)T * k, lines = routed + (has_shared ? T : 0);
   void *scr = nullptr;
   MoeLayout l;
@@ -145,7 +142,7 @@ extern "C" moe_status moe_expert_ffn_mx(moe_ctx *ctx, int dtype, const moe_mx_ex
     return launch_mx_one(ctx, MxOne{x, dtype, experts, topk_idx, topk_w, T, H, I, E, k, has_shared ? 1 : 0, b + o_a, b + o_sa,
                                     out, ctx->dev_small});
   }
-  const size_t o_y = l.take((size_t)lines * H * (y_dtype == MOE_BF16 ? 2 : 4)), o_x = l.take((size_t)T * H / 2),
+  const size_t o_y = l.take((size_t)lines * H * 4), o_x = l.take((size_t)T * H / 2),
                o_sx = l.take((size_t)T * H / kMxBlock), o_counts = l.take(4 * E), o_offsets = l.take(4 * (E + 1)),
                o_perm = l.take(4 * routed);
   if ((st = moe_scratch(ctx, l.size, &scr))) return st;
@@ -161,6 +158,6 @@ extern "C" moe_status moe_expert_ffn_mx(moe_ctx *ctx, int dtype, const moe_mx_ex
   if ((st = launch_mx_gateup(ctx, p, b + o_sa))) return st;
   p.x = b + o_a, p.sx = b + o_sa, p.X = lines, p.N = H, p.K = I, p.tokens = false;
   p.out_rows = p.in_rows, p.in_rows = nullptr, p.out = b + o_y;
-  if ((st = launch_mx_down(ctx, y_dtype, p))) return st;
-  return launch_mx_combine(ctx, y_dtype, dtype, b + o_y, topk_idx, topk_w, T, k, E, H, has_shared, out);
+  if ((st = launch_mx_down(ctx, p))) return st;
+  return launch_mx_combine(ctx, dtype, reinterpret_cast<float *>(b + o_y), topk_idx, topk_w, T, k, E, H, has_shared, out);
 }

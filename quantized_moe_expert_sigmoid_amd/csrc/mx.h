@@ -62,10 +62,10 @@ struct MxOne {
 moe_status launch_mx_one(moe_ctx *ctx, const MxOne &p);
 // silu(x gate^T) * (x up^T) line by line (the table's gate and up), in 4 bits: out's row l is line l
 moe_status launch_mx_gateup(moe_ctx *ctx, const MxProduct &p, uint8_t *scales);
-// the table's down
-moe_status launch_mx_down(moe_ctx *ctx, int dtype, const MxProduct &p);
-moe_status launch_mx_combine(moe_ctx *ctx, int y_dtype, int dtype, const void *y, const int32_t *idx, const float *w,
-                             int T, int k, int E, int H, int has_shared, void *out);
+// the table's down, fp32 results
+moe_status launch_mx_down(moe_ctx *ctx, const MxProduct &p);
+moe_status launch_mx_combine(moe_ctx *ctx, int dtype, const float *y, const int32_t *idx, const float *w, int T, int k, int E,
+                             int H, int has_shared, void *out);
 
 #if defined(__HIPCC__)
 

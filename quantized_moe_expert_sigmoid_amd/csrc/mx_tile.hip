@@ -491,11 +491,8 @@ moe_status launch_mx_gateup(moe_ctx *ctx, const MxProduct &p, uint8_t *scales) {
   MOE_CHECK_LAUNCH("mx gate/up tile kernel");
   return MOE_OK;
 }
-moe_status launch_mx_down(moe_ctx *ctx, int dtype, const MxProduct &p) {
-  if (dtype == MOE_BF16)
-    launch<kDown, MOE_BF16>(ctx, p, nullptr);
-  else
-    launch<kDown, MOE_FP32>(ctx, p, nullptr);
+moe_status launch_mx_down(moe_ctx *ctx, const MxProduct &p) {
+  launch<kDown, MOE_FP32>(ctx, p, nullptr);
   MOE_CHECK_LAUNCH("mx down tile kernel");
   return MOE_OK;
 }

@@ -648,10 +648,11 @@ size_t moe_mx_expert_layout(int H, int I, size_t *offsets_host);
 /* The experts' FFN on hidden states x [T][H] and the combine, in one call:
  *   out[t] = FFN_E(t) (with has_shared) + sum_j topk_w[t][j] FFN_e(t), e =
  *   topk_idx[t][j];  FFN(t) = down q(silu(gate q(x[t])) * (up q(x[t]))),
- * q: to 4 bits as moe_mx_quantize does it. silu(g) = g / (1 + exp(-g)) in fp32 as
- * in moe_expert_ffn_q4; the slots' results are fp32 whatever the type and the
- * number of tokens, and summed in fp32, the shared expert's first, then in slot
- * order; the sum alone is rounded.
+ * q: to 4 bits as moe_mx_quantize does it. silu(g) = g / (1 + exp(-g)) in fp32
+ * with the hardware's exponential and reciprocal, within 2^-21 of the value (2^-148
+ * where that is subnormal); it is not bit for bit moe_expert_ffn_q4's. The slots'
+ * results are fp32 whatever the type and the number of tokens, and summed in fp32,
+ * the shared expert's first, then in slot order; the sum alone is rounded.
  * experts: DEVICE array [E], or [E + 1] with has_shared, whose last entry is the
  * shared expert. x and out (not the same array) are of type dtype. topk_idx int32
  * and topk_w fp32 [T][k] as moe_router_topk gives them. Slots of weight 0 or id

@@ -151,15 +151,21 @@ __device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], uint32_t &byt
 }
 
 // silu(g) = g / (1 + 2^(-g log2 e)) with the hardware's exponential and reciprocal, each within a unit in the last place;
-// the product with log2 e in two parts, since its rounding, times g, is an error of the exponential. Within 2^-21 of the
-// value where that is a normal number. (Exact division and a polynomial: 60 instructions a value, 2 us of a tile's end.)
+// the product with log2 e in two parts, since its rounding, times g, is an error of the exponential. Below -64 both 1 and
+// the exponential are taken 2^-64 times as large, and so in the end the quotient: exp(-g) passes fp32's range at -88.7,
+// silu(g) falls below its normal numbers at -91.8 and below half the smallest number at -108.7. Where |hi| is 192 or more
+// the exponential is 0 or infinite and has no second part (0 or infinity times one is NaN). Within 2^-21 of the value where
+// that is a normal number, else within 2^-148 (every number was tried); -infinity: NaN, as by the formula. (Exact division and a polynomial: 60
+// instructions a value, 2 us of a tile's end.)
 __device__ __forceinline__ float mx_silu(float g) {
   constexpr float kLog2e = 1.4426950408889634f, kRest = (float)(1.4426950408889634074 - (double)kLog2e);
   const float hi = -g * kLog2e, lo = __builtin_fmaf(-g, kRest, __builtin_fmaf(-g, kLog2e, -hi));
-  const float e = __builtin_amdgcn_exp2f(hi);
-  // e (1 + lo ln 2); an infinite e stays so
-  const float d = 1.0f + (lo < 1.0f && lo > -1.0f ? __builtin_fmaf(e, lo * 0.6931471805599453f, e) : e);
-  return g * __builtin_amdgcn_rcpf(d);
+  const bool far = g < -64.0f;
+  const float one = far ? 0x1p-64f : 1.0f;
+  const float e = __builtin_amdgcn_exp2f(far ? hi - 64.0f : hi);  // hi - 64 is exact: smaller than hi, a multiple of its last place
+  // e (1 + lo ln 2)
+  const float d = one + (__builtin_fabsf(hi) < 192.0f ? __builtin_fmaf(e, lo * 0.6931471805599453f, e) : e);
+  return g * __builtin_amdgcn_rcpf(d) * one;
 }
 
 // c += a b^T with v_mfma_scale_f32_16x16x128_f8f6f4: lane l holds block l / 16 (of four) of row l % 16 of a and of b and

@@ -670,7 +670,7 @@ moe_status moe_expert_ffn_mx(moe_ctx *ctx, int dtype, const moe_mx_expert_w *exp
 /* Kernel stages the library times when timing is on. */
 enum {
   MOE_STAGE_ROUTER = 0,   /* activation quantisation + router (+ top-k) */
-  MOE_STAGE_BUCKET = 1,   /* per-expert bucketing */
+  MOE_STAGE_BUCKET = 1,   /* per-expert bucketing (moe_expert_ffn_mx: with the quantiser) */
   MOE_STAGE_GATEUP = 2,   /* gate/up GEMV with the SwiGLU epilogue */
   MOE_STAGE_REQUANT = 3,  /* int8 requantisation of the intermediate (several tokens) */
   MOE_STAGE_DOWN = 4,     /* down GEMV (one token: with the requantisation and the combine) */

@@ -215,8 +215,12 @@ moe_status launch_mx_dequantize(moe_ctx *ctx, int dtype, const uint8_t *codes, c
 moe_status launch_mx_prep(moe_ctx *ctx, int dtype, const void *x, int T, int H, uint8_t *codes, uint8_t *scales,
                           const int32_t *idx, int k, int E, int32_t *counts, int32_t *offsets, int32_t *perm) {
   if ((int64_t)T * k > kPrepEntries) {  // more than one workgroup buckets well
-    moe_status st = launch_mx_quantize(ctx, dtype, x, T, H, H, codes, scales);
-    return st ? st : launch_bucket_public(ctx, idx, T, k, E, counts, offsets, perm);
+    {
+      MoeTimer tm_(ctx, MOE_STAGE_BUCKET);
+      moe_status st = launch_mx_quantize(ctx, dtype, x, T, H, H, codes, scales);
+      if (st) return st;
+    }
+    return launch_bucket_public(ctx, idx, T, k, E, counts, offsets, perm);
   }
   switch (dtype) {
     case MOE_FP32: return prep<MOE_FP32>(ctx, x, T, H, codes, scales, idx, k, E, offsets, perm);

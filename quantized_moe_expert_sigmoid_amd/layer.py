@@ -4,12 +4,17 @@ The hot path of a call (all on the context stream, no host round trip):
     moe_quantize_act_i8 -> moe_router_topk -> moe_expert_ffn_q{4,8,2}
     -> moe_combine
 Weights enter as fp32 host arrays and are quantised and packed on the GPU
-(moe_quantize_rows) straight into contiguous per-expert blocks.
+(moe_quantize_rows) straight into contiguous per-expert blocks. The calls that
+set them are ordered with the caller's current stream, both ways; what forward
+takes and returns is the context stream's, and a caller on another stream orders
+the two.
 
 bits="mx" keeps the experts in microscaled 4-bit floating point instead:
     moe_router_topk -> moe_expert_ffn_mx
 """
 from __future__ import annotations
+
+import contextlib
 
 import numpy as np
 import torch
@@ -45,20 +50,39 @@ class MoeLayer:
         self._bufs = {}
 
     # -- weights -----------------------------------------------------------
+    @contextlib.contextmanager
+    def _ordered(self):
+        """The context's stream after the caller's so far, then the caller's after it: fp32 copies are made on the
+        caller's stream, which may have their memory again as soon as they are dropped."""
+        stream, caller = self.ctx.stream, torch.cuda.current_stream(self.ctx.device)
+        if stream != caller:
+            stream.wait_stream(caller)
+        try:
+            yield
+        finally:
+            if stream != caller:
+                caller.wait_stream(stream)
+
+    def _pack(self, blocks, e: int, *mats):
+        mats = [_to_dev(m, self.device) for m in mats]
+        with self._ordered():
+            blocks.pack_from_fp32(self.ctx, e, *mats)
+
     def set_expert_fp32(self, e: int, wg, wu, wd):
         if self.bits == "mx" and not 0 <= e < self.E:
             raise IndexError(f"expert {e} of {self.E}")
-        self.experts.pack_from_fp32(self.ctx, e, _to_dev(wg, self.device), _to_dev(wu, self.device),
-                                    _to_dev(wd, self.device))
+        self._pack(self.experts, e, wg, wu, wd)
 
     def set_shared_fp32(self, wg, wu, wd):
         blocks, e = (self.experts, self.E) if self.bits == "mx" and self.has_shared else (self.shared, 0)
-        blocks.pack_from_fp32(self.ctx, e, _to_dev(wg, self.device), _to_dev(wu, self.device),
-                              _to_dev(wd, self.device))
+        self._pack(blocks, e, wg, wu, wd)
 
     def set_router(self, w_router, bias=None):
+        old = self.w_router, self.bias
         self.w_router = _to_dev(w_router, self.device)
         self.bias = None if bias is None else _to_dev(bias, self.device)
+        with self._ordered():
+            del old  # calls that read them may still be on their way
 
     # -- buffers -----------------------------------------------------------
     def buffers(self, T: int):

@@ -155,8 +155,8 @@ __device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], uint32_t &byt
 // the exponential are taken 2^-64 times as large, and so in the end the quotient: exp(-g) passes fp32's range at -88.7,
 // silu(g) falls below its normal numbers at -91.8 and below half the smallest number at -108.7. Where |hi| is 192 or more
 // the exponential is 0 or infinite and has no second part (0 or infinity times one is NaN). Within 2^-21 of the value where
-// that is a normal number, else within 2^-148 (every number was tried); -infinity: NaN, as by the formula. (Exact division and a polynomial: 60
-// instructions a value, 2 us of a tile's end.)
+// that is a normal number, else within 2^-148 (every number was tried); -infinity: NaN, as by the formula. (Exact division
+// and a polynomial: 60 instructions a value, 2 us of a tile's end.)
 __device__ __forceinline__ float mx_silu(float g) {
   constexpr float kLog2e = 1.4426950408889634f, kRest = (float)(1.4426950408889634074 - (double)kLog2e);
   const float hi = -g * kLog2e, lo = __builtin_fmaf(-g, kRest, __builtin_fmaf(-g, kLog2e, -hi));

@@ -18,10 +18,12 @@
 // present one begins, and a stage's place is loaded again while its last products
 // run: STAGES - 1 stages are in flight.
 //
-// 2048 lines, 24576 rows of 6144: 185 us, 3.34 PFLOP/s (without the products 146,
-// without the loads 138: the loads bound it, at the rate at which they write LDS).
-// 2047 tokens of 8 of 256 experts of 4096 rows of 6144: 768 us, without the products
-// 758: the weights' bytes.
+// 2048 lines, 24576 rows of 6144: 187 us, 3.3 PFLOP/s (without the products 146,
+// without the loads 138: neither hides the other whole). The 1.2 GB that are
+// loaded, 0.25 of them from memory, come at 32 KB a us and CU where nothing else is
+// done.
+// 2047 tokens of 8 of 256 experts of 4096 rows of 6144: 769 us, without the products
+// 758: 4.2 GB read (3.4 GB are distinct) at 5.4 TB/s, a plain read's rate being 6.3.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -406,10 +408,12 @@ void run(moe_ctx *ctx, const MxProduct &p, uint8_t *a_scales) {
 
 // The tiles there are, lines x rows of weights (gate/up: half as many of each). For a step of 256 k a workgroup takes
 // `full` us where every CU has its `per_cu` workgroups, less with fewer, and `alone` us where a CU has one (measured
-// with 24576, 8192, 6144 and 4096 rows of 2048 to 8192 k; the estimates below are within 30% where the weights' bytes
-// are not the bound and put the tiles in the measured order but for differences of 10%). Few lines an expert want few
+// with 24576, 8192, 6144 and 4096 rows of 2048 to 8192 k; the estimates below are within 40% where the weights' bytes
+// are not the bound and put the tiles in the measured order but for differences of 20%). Few lines an expert want few
 // lines a tile (256 experts, 16384 lines of 6144 by 4096: 32 x 128 1074 us, 64 x 128 844, 128 x 128 862, 128 x 256 809,
 // 256 x 256 1043), a full chip large ones (4096 lines of 6144 by 24576: 817, 549, 419, 407, 376 us), little work many.
+// 128 x 128 is for what is between them: 6423 lines of 6144 by 2642 in these five tiles 188, 136, 113, 166 and 166 us, 2805
+// lines of 6656 by 3206 116, 92, 79, 92 and 95, 5088 lines of 8 experts of 7168 by 2124 159, 122, 99, 139 and 174.
 struct Tile {
   int bm, bn, per_cu;
   double full, alone;
